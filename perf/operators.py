@@ -103,15 +103,17 @@ def prepare(case, seed):
     rnd = lambda *sh: torch.randn(sh, generator=g, device="cuda")  # noqa: E731
     if case["op"] in ("logp", "grad"):
         s["logits"], s["tokens"] = _logits(case, g)
-    if case["op"] == "grad":   # what the forward pass left: lse, entropy and the alternatives' indices
+    if case["op"] == "grad":   # what the forward pass left: each row's maximum and log sum, entropy, alternatives
         N, k = case["N"], case["top"]
-        lse, ent = torch.zeros(N, device="cuda"), torch.zeros(N, device="cuda")
+        stats, ent = torch.zeros((N, 2), device="cuda"), torch.zeros(N, device="cuda")
         for a in range(0, N, 256):
-            z = s["logits"][a:a + 256].double() / case["T"]
-            lse[a:a + 256] = torch.logsumexp(z, -1)
-            p = torch.exp(z - lse[a:a + 256, None])
-            ent[a:a + 256] = -(torch.where(p > 0, z - lse[a:a + 256, None], 0.0) * p).nan_to_num(0.0).sum(-1)
-        s["lse"], s["entropy"] = lse, ent
+            l = s["logits"][a:a + 256].double()
+            m = l.amax(-1)
+            z = (l - m[:, None]) / case["T"]
+            stats[a:a + 256, 0], stats[a:a + 256, 1] = m, torch.logsumexp(z, -1)
+            lp = torch.log_softmax(z, -1)
+            ent[a:a + 256] = -(lp.exp() * lp.clamp(min=-1e300)).sum(-1).nan_to_num(0.0)
+        s["stats"], s["entropy"] = stats, ent
         s["g_logp"], s["g_entropy"] = rnd(N), 0.1 * rnd(N)
         s["top_idx"] = torch.randint(0, case["V"], (N, k), generator=g, device="cuda", dtype=torch.int32) if k else None
         s["g_top"] = 0.2 * rnd(N, k) if k else None
@@ -145,8 +147,8 @@ def _ordered(x):
 
 def _plain_logp(s):
     l, tok, k, V = s["logits"].float(), s["tokens"], s["top"], s["V"]
-    z = l * (1.0 / s["T"])
-    m = z.amax(-1, keepdim=True)
+    ml = l.amax(-1, keepdim=True)
+    z, m = l * (1.0 / s["T"]), ml * (1.0 / s["T"])
     none = torch.isinf(m)[:, 0]   # no unmasked token in the row
     d = z - torch.where(torch.isinf(m), 0.0, m)
     e = torch.exp(d)
@@ -154,12 +156,12 @@ def _plain_logp(s):
     logS = torch.log(S)
     ed = torch.where(e > 0, e * d, 0.0).sum(-1, dtype=torch.float64)
     live = tok >= 0
-    lse = torch.where(live, (m[:, 0].double() + logS).float(), 0.0)
     ent = torch.where(live & ~none, (logS - ed / S).float(), 0.0)
     zt = l.gather(1, tok.clamp(min=0).long()[:, None])[:, 0] * (1.0 / s["T"])
     logp = torch.where(none, -math.inf, ((zt - m[:, 0]).double() - logS).float())
     logp = torch.where(live, logp, 0.0)
-    out = {"logp": logp, "entropy": ent, "lse": lse}
+    stats = torch.where(live[:, None], torch.stack((ml[:, 0], logS.float()), 1), 0.0)
+    out = {"logp": logp, "entropy": ent, "stats": stats}
     if k:
         key = (_ordered(l).long() << 32) | (V - 1 - torch.arange(V, device=l.device))
         idx = V - 1 - (torch.topk(key, k, -1).values & 0xFFFFFFFF)
@@ -173,9 +175,9 @@ def _plain_logp(s):
 
 def _plain_grad(s):
     l, tok = s["logits"], s["tokens"]
-    z = l.float() * (1.0 / s["T"])
-    fine = (tok >= 0) & torch.isfinite(s["lse"])
-    lp = z - torch.where(fine, s["lse"], 0.0)[:, None]
+    m, logS = s["stats"][:, :1], s["stats"][:, 1:]
+    fine = (tok >= 0) & torch.isfinite(m[:, 0])
+    lp = (l.float() - m) * (1.0 / s["T"]) - logS
     p = torch.exp(lp)
     G = torch.where(fine, s["g_logp"] if s["g_top"] is None else s["g_logp"] + s["g_top"].sum(-1), 0.0)
     gH = torch.where(fine, s["g_entropy"], 0.0)
@@ -212,11 +214,11 @@ def _own(s):
 
     op = s["op"]
     if op == "logp":
-        logp, ent, lse, ti, tl = D.token_logprobs(s["logits"], s["tokens"], s["T"], top=s["top"])
-        out = {"logp": logp, "entropy": ent, "lse": lse}
+        logp, ent, ti, tl, stats = D.token_logprobs(s["logits"], s["tokens"], s["T"], top=s["top"])
+        out = {"logp": logp, "entropy": ent, "stats": stats}
         return {**out, "top_idx": ti, "top_logp": tl} if s["top"] else out
     if op == "grad":
-        return {"grad": D.token_logprobs_backward(s["logits"], s["tokens"], s["T"], s["lse"], s["entropy"],
+        return {"grad": D.token_logprobs_backward(s["logits"], s["tokens"], s["T"], s["stats"], s["entropy"],
                                                   s["g_logp"], s["g_entropy"], top_idx=s["top_idx"],
                                                   g_top=s["g_top"])}
     if op == "norm":
@@ -239,10 +241,10 @@ def work(case):
     operations an element takes. A row without a token need not be read (its gradient is written)."""
     if case["op"] == "logp":
         n, b = case["N"] - case["pad"], _SIZE[case["dtype"]]
-        return {"bytes": n * case["V"] * b + case["N"] * (16 + 8 * case["top"]), "flops": 5 * n * case["V"]}
+        return {"bytes": n * case["V"] * b + case["N"] * (20 + 8 * case["top"]), "flops": 5 * n * case["V"]}
     if case["op"] == "grad":
         b = _SIZE[case["dtype"]]
-        return {"bytes": (2 * case["N"] - case["pad"]) * case["V"] * b + case["N"] * (20 + 8 * case["top"]),
+        return {"bytes": (2 * case["N"] - case["pad"]) * case["V"] * b + case["N"] * (24 + 8 * case["top"]),
                 "flops": 6 * (case["N"] - case["pad"]) * case["V"]}
     if case["op"] == "norm":
         b = _SIZE[case["dtype"]]
@@ -258,7 +260,7 @@ def exact(case, seed):
     s = prepare(case, seed)
     if case["op"] == "logp":
         N, k = case["N"], case["top"]
-        f = {n: [] for n in ("logp", "entropy", "lse", "top_logp")}
+        f = {n: [] for n in ("logp", "entropy", "stats", "top_logp")}
         for a in range(0, N, 256):
             t = s["tokens"][a:a + 256].long()
             z = s["logits"][a:a + 256].double() / case["T"]
@@ -271,7 +273,9 @@ def exact(case, seed):
             H = -(p * lp.clamp(min=-1e300)).sum(-1)
             f["logp"].append(at.masked_fill(dead, 0))
             f["entropy"].append(H.masked_fill(dead | void, 0))
-            f["lse"].append(lse.masked_fill(dead, 0))
+            m = s["logits"][a:a + 256].double().amax(-1)
+            logS = torch.where(void, -math.inf, lse - m / case["T"])
+            f["stats"].append(torch.stack((m, logS), 1).masked_fill(dead[:, None], 0))
             if k:
                 f["top_logp"].append(torch.sort(lp, -1, descending=True).values[:, :k].masked_fill(dead[:, None], -math.inf))
         out = {n: torch.cat(v) for n, v in f.items() if v}
