@@ -49,8 +49,8 @@ typedef enum {
   DSPARK_ETIMEOUT = 4   /* a bounded device wait gave up (read through dspark_workspace_status) */
 } dspark_status;
 
-/* weight dtypes */
-enum { DSPARK_F32 = 0, DSPARK_BF16 = 1 };
+/* dtypes of weights, logits and hidden states (each entry point says which it takes) */
+enum { DSPARK_F32 = 0, DSPARK_BF16 = 1, DSPARK_F16 = 2 };
 
 /* layouts of the draft logits U and l_d (rows of V fp32 values):
  *   DSPARK_POSITION_MAJOR  [gamma, B, V]: step k of the draft reads and writes one contiguous
@@ -403,6 +403,66 @@ int dspark_prefix_schedule(const float* c, const double* sps, int B, int gamma, 
 int dspark_prefix_schedule_t2(const float* c, const double* sps, int B, int gamma, int D_max, int mode,
                               int K_init, void* ring, int32_t* L_out, float* a_out, double* theta_out,
                               int32_t* K_out, uint32_t* flags, void* stream);
+
+/* --------------------------------------------------------------------------
+ * dspark_token_logprobs -- log probabilities of given tokens, with entropy and top alternatives.
+ *
+ * The pages end a round at the emitted tokens; what a serving interface returns for them, and what
+ * a trainer of the draft head learns from, is their log probability under a row of logits (target
+ * rows l_t, padded or flattened, or draft rows l_d).  For entry n with row l and z = l / T:
+ *     logp[n]      = z_tok - log sum_v exp z_v
+ *     entropy[n]   = - sum_v p_v log p_v,   p = softmax(z)
+ *     top_idx[n,:] = the `top` largest logits, value descending, lowest index first on ties;
+ *     top_logp[n,:]  their log probabilities
+ *     stats[n]     = (m, log sum_v exp((l_v - m) / T)),  m = max_v l_v  (for the backward pass; the
+ *                    row's log sum exp is m / T + stats[n][1])
+ * -Inf is a masked token: it is no alternative (the places left over hold -1 and -Inf), and as the
+ * given token it has logp -Inf.  The type's lowest value is an ordinary logit.  A row in which
+ * everything is masked has logp -Inf, entropy 0 and stats (-Inf, -Inf).  A row with NaN or +Inf has
+ * NaN everywhere and no alternatives (-1); NONFINITE is set.
+ *
+ * logits   [n_rows, V], dtype DSPARK_F32, DSPARK_BF16 or DSPARK_F16, rows `ld` elements apart
+ *          (ld >= V; any alignment of the element type).
+ * rows     [N] int64 row of each entry, or NULL: entry n reads row n (then N <= n_rows).  A row may be
+ *          read by several entries.  For y of dspark_verify_ragged, entry (b, k) has row lt_off[b] + k;
+ *          for x over position-major l_d, row k * B + b.  An index outside [0, n_rows) is not read: NaN,
+ *          alternatives -1, and RAGGED_OFFSETS.
+ * tokens   [N] int32.  -1 (as dspark_verify pads y) is an entry without a token: its row is not read
+ *          and it gets logp, entropy and stats 0, alternatives -1 and -Inf.  Any other index outside
+ *          [0, V) has logp NaN and sets TOKEN_RANGE; the entry's other outputs are computed.
+ * T        finite, >= 1e-6.
+ * top      0..DSPARK_TOP_MAX alternatives (may exceed V).
+ * logp     [N] fp32.  entropy [N] fp32 or NULL.  top_idx [N, top] int32 and top_logp [N, top] fp32
+ *          (required when top > 0).  stats [N, 2] fp32 or NULL, 8-byte aligned.
+ * flags    [N] uint32 or NULL, OR'ed with NONFINITE / TOKEN_RANGE / RAGGED_OFFSETS of each entry.
+ * Sums are fp32 per lane, joined in fp64; results do not depend on timing.  N = 0 does nothing.
+ * Limits: V <= 2^24, N <= 2^26.  No workspace.
+ * -------------------------------------------------------------------------- */
+#define DSPARK_TOP_MAX 32
+int dspark_token_logprobs(const void* logits, int dtype, int64_t ld, int64_t n_rows, const int64_t* rows,
+                          const int32_t* tokens, int N, int V, float T, int top, float* logp, float* entropy,
+                          int32_t* top_idx, float* top_logp, float* stats, uint32_t* flags, void* stream);
+
+/* --------------------------------------------------------------------------
+ * dspark_token_logprobs_backward -- gradient of dspark_token_logprobs with respect to the logits.
+ *
+ *     grad[n,v] = ( g_logp[n] [v == tok] + sum_j g_top[n,j] [v == top_idx[n,j]]
+ *                   - p_v ( G + g_entropy[n] (log p_v + entropy[n]) ) ) / T,
+ *     G = g_logp[n] + sum_j g_top[n,j]
+ * formed in fp32 and rounded once to dtype.  Entry n is row n of the logits.  Alternatives with index
+ * -1 take no part; the same index may occur several times.  Rows without a token (index outside
+ * [0, V)) and rows in which everything is masked have gradient 0; rows with NaN or +Inf have NaN.
+ * stats     [N, 2] fp32 of the forward call (8-byte aligned); entropy [N] (required with g_entropy).
+ * g_logp    [N] fp32 or NULL (0).  g_entropy [N] fp32 or NULL (0).
+ * top_idx   [N, top] int32 and g_top [N, top] fp32, required when top > 0.
+ * grad      [N, V] of the logits' dtype, rows ldg elements apart.  It may be the logits themselves
+ *           (same address and ldg == ld); any other overlap is refused.
+ * Other arguments as dspark_token_logprobs.  No workspace.
+ * -------------------------------------------------------------------------- */
+int dspark_token_logprobs_backward(const void* logits, int dtype, int64_t ld, const int32_t* tokens, int N, int V,
+                                   float T, const float* stats, const float* entropy, const float* g_logp,
+                                   const float* g_entropy, int top, const int32_t* top_idx, const float* g_top,
+                                   void* grad, int64_t ldg, void* stream);
 
 #ifdef __cplusplus
 }

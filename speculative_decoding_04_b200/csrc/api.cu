@@ -83,6 +83,10 @@ int device_sm_count() {
   return n;
 }
 
+static size_t dtype_bytes(int dtype) {
+  return dtype == DSPARK_F32 ? 4 : dtype == DSPARK_BF16 || dtype == DSPARK_F16 ? 2 : 0;
+}
+
 static dspark_status einval(const std::string& msg) {
   set_error(msg);
   return DSPARK_EINVAL;
@@ -306,6 +310,58 @@ int dspark_prefix_schedule_t2(const float* c, const double* sps, int B, int gamm
   s.K_init = K_init;
   s.K_out = K_out;
   return launch_schedule(s);
+}
+
+int dspark_token_logprobs(const void* logits, int dtype, int64_t ld, int64_t n_rows, const int64_t* rows,
+                          const int32_t* tokens, int N, int V, float T, int top, float* logp, float* entropy,
+                          int32_t* top_idx, float* top_logp, float* stats, uint32_t* flags, void* stream) {
+  const size_t es = dtype_bytes(dtype);
+  if (!es) return einval("dspark_token_logprobs: dtype must be DSPARK_F32, DSPARK_BF16 or DSPARK_F16");
+  if (N < 0 || V < 1) return einval("dspark_token_logprobs: N must be >= 0 and V >= 1");
+  if (V > kMaxLogprobsV) return einval("dspark_token_logprobs: V must be <= 2^24");
+  if (ld < V) return einval("dspark_token_logprobs: ld must be >= V");
+  if (n_rows < 0 || (!rows && n_rows < N)) return einval("dspark_token_logprobs: fewer rows than entries");
+  if (n_rows > 0 && ld > INT64_MAX / 8 / n_rows) return einval("dspark_token_logprobs: tensor too large");
+  if (!(T >= 1e-6f) || std::isinf(T)) return einval("dspark_token_logprobs: T must be finite and >= 1e-6");
+  if (top < 0 || top > DSPARK_TOP_MAX) return einval("dspark_token_logprobs: top must be in [0, 32]");
+  if (N == 0) return DSPARK_OK;
+  if (!logits || !tokens || !logp) return einval("dspark_token_logprobs: null pointer");
+  if (top > 0 && (!top_idx || !top_logp)) return einval("dspark_token_logprobs: top_idx and top_logp are required when top > 0");
+  if ((uintptr_t)logits % es) return einval("dspark_token_logprobs: logits must be aligned to their type");
+  if ((uintptr_t)stats % 8) return einval("dspark_token_logprobs: stats must be 8-byte aligned");
+  if (N > kMaxLogprobsN) return einval("dspark_token_logprobs: N must be <= 2^26");
+  LogprobsCall c{logits, dtype, ld, n_rows, rows, tokens, N, V, T, top, logp, entropy, top_idx, top_logp, stats, flags,
+                 (cudaStream_t)stream};
+  return launch_token_logprobs(c);
+}
+
+int dspark_token_logprobs_backward(const void* logits, int dtype, int64_t ld, const int32_t* tokens, int N, int V,
+                                   float T, const float* stats, const float* entropy, const float* g_logp,
+                                   const float* g_entropy, int top, const int32_t* top_idx, const float* g_top,
+                                   void* grad, int64_t ldg, void* stream) {
+  const size_t es = dtype_bytes(dtype);
+  if (!es) return einval("dspark_token_logprobs_backward: dtype must be DSPARK_F32, DSPARK_BF16 or DSPARK_F16");
+  if (N < 0 || V < 1) return einval("dspark_token_logprobs_backward: N must be >= 0 and V >= 1");
+  if (V > kMaxLogprobsV) return einval("dspark_token_logprobs_backward: V must be <= 2^24");
+  if (ld < V || ldg < V) return einval("dspark_token_logprobs_backward: ld and ldg must be >= V");
+  if (N > 0 && (ld > INT64_MAX / 8 / N || ldg > INT64_MAX / 8 / N))
+    return einval("dspark_token_logprobs_backward: tensor too large");
+  if (!(T >= 1e-6f) || std::isinf(T)) return einval("dspark_token_logprobs_backward: T must be finite and >= 1e-6");
+  if (top < 0 || top > DSPARK_TOP_MAX) return einval("dspark_token_logprobs_backward: top must be in [0, 32]");
+  if (N == 0) return DSPARK_OK;
+  if (!logits || !tokens || !stats || !grad) return einval("dspark_token_logprobs_backward: null pointer");
+  if (g_entropy && !entropy) return einval("dspark_token_logprobs_backward: entropy is required with g_entropy");
+  if (top > 0 && (!top_idx || !g_top)) return einval("dspark_token_logprobs_backward: top_idx and g_top are required when top > 0");
+  if ((uintptr_t)logits % es || (uintptr_t)grad % es)
+    return einval("dspark_token_logprobs_backward: logits and grad must be aligned to their type");
+  if ((uintptr_t)stats % 8) return einval("dspark_token_logprobs_backward: stats must be 8-byte aligned");
+  const char *l0 = static_cast<const char*>(logits), *g0 = static_cast<const char*>(grad);
+  const char *l1 = l0 + ((size_t)(N - 1) * ld + V) * es, *g1 = g0 + ((size_t)(N - 1) * ldg + V) * es;
+  if (l0 < g1 && g0 < l1 && !(l0 == g0 && ld == ldg))
+    return einval("dspark_token_logprobs_backward: grad overlaps the logits without being them");
+  LogprobsBwdCall c{logits, dtype, ld, tokens, N, V, T, stats, entropy, g_logp, g_entropy, top, top_idx, g_top, grad, ldg,
+                    (cudaStream_t)stream};
+  return launch_token_logprobs_backward(c);
 }
 
 }  // extern "C"

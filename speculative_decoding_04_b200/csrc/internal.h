@@ -134,6 +134,45 @@ struct ScheduleCall {
   int32_t* K_out = nullptr;
 };
 
+struct LogprobsCall {
+  const void* logits;
+  int dtype;
+  long long ld, n_rows;
+  const int64_t* rows;
+  const int32_t* tokens;
+  int N, V;
+  float T;
+  int top;
+  float* logp;
+  float* entropy;
+  int32_t* top_idx;
+  float* top_logp;
+  float* stats;
+  uint32_t* flags;
+  cudaStream_t stream;
+};
+dspark_status launch_token_logprobs(const LogprobsCall& c);
+
+struct LogprobsBwdCall {
+  const void* logits;
+  int dtype;
+  long long ld;
+  const int32_t* tokens;
+  int N, V;
+  float T;
+  const float* stats;
+  const float* entropy;
+  const float* g_logp;
+  const float* g_entropy;
+  int top;
+  const int32_t* top_idx;
+  const float* g_top;
+  void* grad;
+  long long ldg;
+  cudaStream_t stream;
+};
+dspark_status launch_token_logprobs_backward(const LogprobsBwdCall& c);
+
 size_t draft_workspace_bytes(int B, int gamma, int V, int r);
 size_t rnn_draft_workspace_bytes(int B, int gamma, int V, int r);
 size_t verify_workspace_bytes(int B, int gamma, int V);
@@ -149,6 +188,8 @@ dspark_status launch_schedule(const ScheduleCall& c);
 
 constexpr int kMaxGamma = 64;
 constexpr int kMaxScheduleItems = 16384;
+constexpr int kMaxLogprobsV = 1 << 24;  // tiles of 2 KB, at most 4096 of them for each of 16 CTAs
+constexpr int kMaxLogprobsN = 1 << 26;  // 16 CTAs each
 constexpr size_t kWsHeader = 256;
 
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }

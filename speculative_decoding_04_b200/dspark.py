@@ -20,12 +20,13 @@ import torch
 from .build import LIB_PATH, ROOT
 
 OK, EINVAL, ECUDA, ENOTIMPL, ETIMEOUT = 0, 1, 2, 3, 4
-F32, BF16 = 0, 1
+F32, BF16, F16 = 0, 1, 2
 POSITION_MAJOR, REQUEST_MAJOR = 0, 1
 _LAYOUTS = {"position": POSITION_MAJOR, "request": REQUEST_MAJOR}
 SCHED_ARGMAX, SCHED_EARLY_STOP = 0, 1
 WS_DRAFT, WS_VERIFY, WS_SCHEDULE, WS_RNN_DRAFT = 0, 1, 2, 3
 T2_RING_BYTES = 128
+TOP_MAX = 32
 
 FLAG_DRAFT_NEAR_TIE = 1 << 0
 FLAG_ACCEPT_NEAR_TIE = 1 << 1
@@ -48,6 +49,8 @@ class DsparkError(RuntimeError):
 
 
 _vp, _i, _f, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+_i64 = ctypes.c_int64
+_DTYPES = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
 
 
 def _load() -> ctypes.CDLL:
@@ -91,6 +94,12 @@ def _load() -> ctypes.CDLL:
                                          _vp, _vp, _vp, _vp, _sz, _vp]
     lib.dspark_prefix_schedule_t2.restype = _i
     lib.dspark_prefix_schedule_t2.argtypes = [_vp, _vp, _i, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp]
+    lib.dspark_token_logprobs.restype = _i
+    lib.dspark_token_logprobs.argtypes = [_vp, _i, _i64, _i64, _vp, _vp, _i, _i, _f, _i, _vp, _vp, _vp, _vp, _vp, _vp,
+                                          _vp]
+    lib.dspark_token_logprobs_backward.restype = _i
+    lib.dspark_token_logprobs_backward.argtypes = [_vp, _i, _i64, _vp, _i, _i, _f, _vp, _vp, _vp, _vp, _i, _vp, _vp,
+                                                   _vp, _i64, _vp]
     return lib
 
 
@@ -453,3 +462,139 @@ def prefix_schedule_t2(c: torch.Tensor, sps: torch.Tensor, D_max: int, ring: tor
                                        _p(L_out), _p(a_out), _p(theta_out), _p(K_out), _p(flags), _s(stream))
     _check("dspark_prefix_schedule_t2", st)
     return L_out, a_out, theta_out, K_out, flags
+
+
+def _rows2d(t: torch.Tensor, name: str) -> torch.Tensor:
+    """t as [rows, columns] without a copy: columns dense, rows a constant stride apart."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype not in _DTYPES:
+        raise ValueError(f"{name} must be fp32, bf16 or fp16, got {t.dtype}")
+    if t.dim() < 2:
+        raise ValueError(f"{name} must have at least 2 dimensions")
+    if t.dim() > 2:
+        try:
+            t = t.view(-1, t.shape[-1])
+        except RuntimeError as e:
+            raise ValueError(f"{name}: the rows of {tuple(t.shape)} are not a constant stride apart") from e
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: the last dimension must be dense")
+    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+        raise ValueError(f"{name}: rows must not overlap")
+    return t
+
+
+def _ld(t: torch.Tensor) -> int:
+    """Row stride of a tensor that passed _rows2d (a single row's stride says nothing)."""
+    return t.stride(0) if t.shape[0] > 1 else max(1, t.shape[1])
+
+
+def _arg(t: Optional[torch.Tensor], name: str, dtype, numel: int, dev) -> Optional[ctypes.c_void_p]:
+    """The address of a contiguous argument of `numel` values on `dev` (None stays None)."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev}, got {t.device}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.numel() != numel or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous with {numel} values, got {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _elsewhere(dev, stream) -> bool:
+    """The call is not for the current device and its current stream."""
+    return stream is not None or dev.index != torch.cuda.current_device()
+
+
+def _at(fn, dev, stream, *args, **kw):
+    """fn with `dev` current and `stream` (or dev's current stream) as its current stream, so that what
+    it allocates belongs to the stream that uses it."""
+    with torch.cuda.device(dev), torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(dev)):
+        return fn(*args, **kw)
+
+
+def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, T: float = 1.0, *, top: int = 0, rows=None, logp=None,
+                   entropy=None, top_idx=None, top_logp=None, stats=None, flags=None, stream=None):
+    """Log probabilities of `tokens` under rows of `logits` at temperature T, with entropy and the
+    `top` most likely alternatives.
+
+    logits [..., V] (fp32, bf16 or fp16; leading dimensions are rows a constant stride apart); tokens
+    int32 of any shape with N values, entry n under row n, or under row rows[n] (int64, as many values
+    as tokens).  -1 is an entry without a token.  Returns (logp, entropy, top_idx, top_logp, stats):
+    logp and entropy shaped as tokens, the alternatives [..., top] (None when top is 0), stats [..., 2]
+    for token_logprobs_backward.  flags: int32, one word per entry, zeroed by the caller, or None."""
+    l2 = _rows2d(logits, "logits")
+    dev = l2.device
+    if _elsewhere(dev, stream):
+        return _at(token_logprobs, dev, stream, logits, tokens, T, top=top, rows=rows, logp=logp, entropy=entropy,
+                   top_idx=top_idx, top_logp=top_logp, stats=stats, flags=flags)
+    top = int(top)
+    N, V = tokens.numel(), l2.shape[1]
+    shape = tuple(tokens.shape)
+    if logp is None:
+        logp = torch.empty(shape, dtype=torch.float32, device=dev)
+    if entropy is None:
+        entropy = torch.empty(shape, dtype=torch.float32, device=dev)
+    if stats is None:
+        stats = torch.empty(shape + (2,), dtype=torch.float32, device=dev)
+    if top > 0:
+        if top_idx is None:
+            top_idx = torch.empty(shape + (top,), dtype=torch.int32, device=dev)
+        if top_logp is None:
+            top_logp = torch.empty(shape + (top,), dtype=torch.float32, device=dev)
+    else:
+        top_idx = top_logp = None
+    st = lib.dspark_token_logprobs(
+        l2.data_ptr(), _DTYPES[l2.dtype], _ld(l2), l2.shape[0], _arg(rows, "rows", torch.int64, N, dev),
+        _arg(tokens, "tokens", torch.int32, N, dev), N, V, float(T), top, _arg(logp, "logp", torch.float32, N, dev),
+        _arg(entropy, "entropy", torch.float32, N, dev), _arg(top_idx, "top_idx", torch.int32, N * top, dev),
+        _arg(top_logp, "top_logp", torch.float32, N * top, dev), _arg(stats, "stats", torch.float32, 2 * N, dev),
+        _arg(flags, "flags", torch.int32, N, dev), torch.cuda.current_stream().cuda_stream)
+    _check("dspark_token_logprobs", st)
+    return logp, entropy, top_idx, top_logp, stats
+
+
+def token_logprobs_backward(logits: torch.Tensor, tokens: torch.Tensor, T: float, stats: torch.Tensor,
+                            entropy: Optional[torch.Tensor], g_logp: Optional[torch.Tensor],
+                            g_entropy: Optional[torch.Tensor] = None, *, top_idx=None, g_top=None, grad=None,
+                            stream=None) -> torch.Tensor:
+    """Gradient of token_logprobs (entry n = row n) with respect to the logits.
+
+    stats, entropy: what the forward call returned; g_logp, g_entropy and g_top ([..., top], with the
+    forward's top_idx): the gradients of its outputs, each or None.  grad: where to write it -- the
+    logits' dtype and shape, the logits themselves among them -- or None: a new tensor with the strides
+    of the logits' rows."""
+    l2 = _rows2d(logits, "logits")
+    dev = l2.device
+    if _elsewhere(dev, stream):
+        return _at(token_logprobs_backward, dev, stream, logits, tokens, T, stats, entropy, g_logp, g_entropy,
+                   top_idx=top_idx, g_top=g_top, grad=grad)
+    N, V = l2.shape
+    if tokens.numel() != N:
+        raise ValueError(f"tokens must have one value per row, {N}, got {tokens.numel()}")
+    if (top_idx is None) != (g_top is None):
+        raise ValueError("top_idx and g_top come together")
+    if top_idx is not None and N and top_idx.numel() % N:
+        raise ValueError("top_idx must be [..., top]")
+    top = top_idx.numel() // N if top_idx is not None and N else 0
+    if grad is None:
+        out = torch.empty_strided((N, V), (_ld(l2), 1), dtype=l2.dtype, device=dev)
+        grad = out.view(logits.shape) if logits.dim() > 2 else out
+        g2 = out
+    else:
+        g2 = _rows2d(grad, "grad")
+        if grad.device != dev or grad.dtype != l2.dtype or grad.shape != logits.shape:
+            raise ValueError(f"grad must be {l2.dtype} {tuple(logits.shape)} on {dev}")
+    st = lib.dspark_token_logprobs_backward(
+        l2.data_ptr(), _DTYPES[l2.dtype], _ld(l2), _arg(tokens, "tokens", torch.int32, N, dev), N, V, float(T),
+        _arg(stats, "stats", torch.float32, 2 * N, dev), _arg(entropy, "entropy", torch.float32, N, dev),
+        _arg(g_logp, "g_logp", torch.float32, N, dev), _arg(g_entropy, "g_entropy", torch.float32, N, dev), top,
+        _arg(top_idx, "top_idx", torch.int32, N * top, dev), _arg(g_top, "g_top", torch.float32, N * top, dev),
+        g2.data_ptr(), _ld(g2), torch.cuda.current_stream().cuda_stream)
+    _check("dspark_token_logprobs_backward", st)
+    return grad
