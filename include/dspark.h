@@ -464,6 +464,63 @@ int dspark_token_logprobs_backward(const void* logits, int dtype, int64_t ld, co
                                    const float* g_entropy, int top, const int32_t* top_idx, const float* g_top,
                                    void* grad, int64_t ldg, void* stream);
 
+/* --------------------------------------------------------------------------
+ * dspark_rmsnorm_q8 -- root-mean-square norm with the residual's addition and an 8-bit output.
+ *
+ * The step between a backbone's last layer and its LM head: the head then reads 8-bit rows
+ * (dspark_matmul_q8).  For each row
+ *     h     = x + residual, rounded to dtype (h = x without a residual)
+ *     v     = h * gain (one fp32 product),  A = max |v|
+ *     q     = rint(v * (127 / A))           (fp32 division and product; ties to even)
+ *     scale = A / sqrt(mean h^2 + eps) / 127
+ * so that q * scale is the normalised row times the gain.  The norm's factor is common to the row and
+ * cancels in q.  The sum of squares is fp32.  A row with A < 2^-120 counts as zero (q 0, scale 0); a row
+ * with NaN or an infinity has q 0 and scale NaN, which makes the head's logits of that row NaN.
+ *
+ * x         [M, d] of dtype (DSPARK_F32, DSPARK_BF16 or DSPARK_F16), rows ldx elements apart.
+ * residual  [M, d] of dtype, rows ldr apart, or NULL.
+ * gain      [d] of gain_dtype (dtype itself or DSPARK_F32), or NULL (1).
+ * eps       > 0, finite.
+ * h_out     [M, d] of dtype, rows ldh apart: required with a residual, ignored without.  It may be x
+ *           or the residual itself (same address and stride).
+ * q         [M, d] int8, rows ldq bytes apart (a multiple of 16 for dspark_matmul_q8).
+ * scale     [M] fp32.
+ * M = 0 does nothing.  No workspace.
+ * -------------------------------------------------------------------------- */
+int dspark_rmsnorm_q8(const void* x, int dtype, int64_t ldx, const void* residual, int64_t ldr, const void* gain,
+                      int gain_dtype, int M, int d, float eps, void* h_out, int64_t ldh, int8_t* q, int64_t ldq,
+                      float* scale, void* stream);
+
+/* --------------------------------------------------------------------------
+ * dspark_quantize_q8 -- rows to 8-bit integers with one scale each: A = max |x|,
+ * q = rint(x * (127 / A)), scale = A / 127.  For the weights of dspark_matmul_q8 (once, when they are
+ * loaded) and for activations that need no norm.  Arguments and special rows as dspark_rmsnorm_q8.
+ * -------------------------------------------------------------------------- */
+int dspark_quantize_q8(const void* x, int dtype, int64_t ldx, int M, int d, int8_t* q, int64_t ldq, float* scale,
+                       void* stream);
+
+/* --------------------------------------------------------------------------
+ * dspark_matmul_q8 -- matrix product in 8-bit integers with scales for each token and channel.
+ *
+ * [P1 §"DSpark 架构设计：半自回归生成与马尔可夫修正"] the parallel backbone shares the target's LM head
+ * and emits the base logits of every position in one forward.  This is that head on 8-bit weights:
+ *     out[m,n] = q_scale[m] * w_scale[n] * sum_k q[m,k] * w[n,k]
+ * The sum is exact (int32); it is rounded to fp32 once, multiplied by the scales in fp32 and rounded
+ * once to the output's type.  With out fp32 and the rows m in the order of U ([gamma, B] or [B, gamma])
+ * or of l_t, the output is the input of dspark_markov_draft or dspark_verify.
+ *
+ * q        [M, K] int8, 16-byte aligned, rows ldq bytes apart;  q_scale [M] fp32.
+ * w        [N, K] int8, 16-byte aligned, rows ldw bytes apart;  w_scale [N] fp32.
+ *          ldq and ldw are multiples of 16 (bytes between a row's end and the next are not read).
+ * out      [M, N] of out_dtype (DSPARK_F32, DSPARK_BF16 or DSPARK_F16), rows ldo elements apart.
+ * flags    [M] uint32 or NULL: DEVICE_TIMEOUT where a bounded device wait gave up; the outputs it
+ *          could not compute are then NaN.
+ * Limits: 1 <= K <= 131071.  M = 0 does nothing.  No workspace.
+ * -------------------------------------------------------------------------- */
+int dspark_matmul_q8(const int8_t* q, int64_t ldq, const float* q_scale, const int8_t* w, int64_t ldw,
+                     const float* w_scale, int M, int N, int K, void* out, int out_dtype, int64_t ldo, uint32_t* flags,
+                     void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -11,4 +11,4 @@ from .dspark_oracle import (NEAR_TIE, THETA_NEAR_TIE, SCHED_ARGMAX, SCHED_EARLY_
                             tv_labels_ragged, ECE_BINS, ece, sts_scale, sts_fit, prefix_survival, schedule_order, prefix_schedule,
                             schedule_at_capacity, prefix_schedule_t2,
                             exhaustive_schedule)
-from .operators_oracle import token_logprobs, token_logprobs_grad
+from .operators_oracle import matmul_q8, quantize_q8, rmsnorm_q8, token_logprobs, token_logprobs_grad

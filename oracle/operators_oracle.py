@@ -3,6 +3,9 @@
 Plain float64 NumPy from the operators' definitions, sharing no code with the CUDA path:
   * token_logprobs, token_logprobs_grad -- log softmax at temperature T of given tokens, its entropy
     and largest entries, and the gradient with respect to the logits.
+  * rmsnorm_q8, quantize_q8 -- root-mean-square norm (or none) on an 8-bit grid per row; the grid is
+    defined on fp32 products, so q is reproduced exactly and the scale is fp64.
+  * matmul_q8 -- integer product with a scale for each row of either side.
 """
 
 from __future__ import annotations
@@ -83,3 +86,39 @@ def token_logprobs_grad(logits, tokens, T: float, g_logp=None, g_entropy=None, t
             d -= float(g_entropy[n]) * (plp - p * plp.sum())
         out[n] = d / T
     return out
+
+
+def rmsnorm_q8(h, gain, eps: float):
+    """(q int8 [M, d], scale fp64 [M]) of rows h (already x + residual, rounded to their type).
+
+    v = fp32(h * gain), A = max |v|, q = rint(fp32(v * fp32(127 / A))), scale = A / sqrt(mean h^2 + eps) / 127.
+    A row with A < 2^-120: zeros.  A row with NaN or infinity: q 0, scale NaN."""
+    h32 = np.asarray(h, dtype=np.float32)
+    g = np.ones(h32.shape[1], np.float32) if gain is None else np.asarray(gain, dtype=np.float32)
+    return _to_grid(h32, g, lambda r: 1 / np.sqrt(np.mean(h32[r].astype(np.float64) ** 2) + eps))
+
+
+def quantize_q8(x):
+    """(q int8, scale fp64) of rows: A = max |x|, q = rint(fp32(x * fp32(127 / A))), scale = A / 127."""
+    x32 = np.asarray(x, dtype=np.float32)
+    return _to_grid(x32, np.ones(x32.shape[1], np.float32), lambda r: 1.0)
+
+
+def _to_grid(h, g, factor):
+    q, scale = np.zeros(h.shape, np.int8), np.zeros(h.shape[0])
+    for r in range(h.shape[0]):
+        with np.errstate(all="ignore"):
+            v = h[r] * g
+            A = np.abs(v).max()
+        if not np.isfinite(A) or not np.isfinite(h[r]).all():
+            scale[r] = np.nan
+        elif A >= 2.0 ** -120:
+            q[r] = np.rint(v * (np.float32(127) / A)).astype(np.int8)
+            scale[r] = float(A) * factor(r) / 127
+    return q, scale
+
+
+def matmul_q8(q, q_scale, w, w_scale):
+    """[M, N] fp64: q_scale[m] w_scale[n] sum_k q[m, k] w[n, k] (products of 8-bit integers are exact in fp64)."""
+    s = np.asarray(q, dtype=np.float64) @ np.asarray(w, dtype=np.float64).T
+    return s * np.asarray(q_scale, dtype=np.float64)[:, None] * np.asarray(w_scale, dtype=np.float64)

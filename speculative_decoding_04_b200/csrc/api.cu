@@ -87,6 +87,13 @@ static size_t dtype_bytes(int dtype) {
   return dtype == DSPARK_F32 ? 4 : dtype == DSPARK_BF16 || dtype == DSPARK_F16 ? 2 : 0;
 }
 
+// Two [rows, cols] arrays with element size es share memory without being the same array.
+static bool bad_overlap(const void* a, int64_t lda, const void* b, int64_t ldb, int rows, int cols, size_t es) {
+  const char *a0 = static_cast<const char*>(a), *b0 = static_cast<const char*>(b);
+  const char *a1 = a0 + ((size_t)(rows - 1) * lda + cols) * es, *b1 = b0 + ((size_t)(rows - 1) * ldb + cols) * es;
+  return a0 < b1 && b0 < a1 && !(a0 == b0 && (lda == ldb || rows == 1));
+}
+
 static dspark_status einval(const std::string& msg) {
   set_error(msg);
   return DSPARK_EINVAL;
@@ -355,13 +362,67 @@ int dspark_token_logprobs_backward(const void* logits, int dtype, int64_t ld, co
   if ((uintptr_t)logits % es || (uintptr_t)grad % es)
     return einval("dspark_token_logprobs_backward: logits and grad must be aligned to their type");
   if ((uintptr_t)stats % 8) return einval("dspark_token_logprobs_backward: stats must be 8-byte aligned");
-  const char *l0 = static_cast<const char*>(logits), *g0 = static_cast<const char*>(grad);
-  const char *l1 = l0 + ((size_t)(N - 1) * ld + V) * es, *g1 = g0 + ((size_t)(N - 1) * ldg + V) * es;
-  if (l0 < g1 && g0 < l1 && !(l0 == g0 && ld == ldg))
+  if (bad_overlap(grad, ldg, logits, ld, N, V, es))
     return einval("dspark_token_logprobs_backward: grad overlaps the logits without being them");
   LogprobsBwdCall c{logits, dtype, ld, tokens, N, V, T, stats, entropy, g_logp, g_entropy, top, top_idx, g_top, grad, ldg,
                     (cudaStream_t)stream};
   return launch_token_logprobs_backward(c);
+}
+
+int dspark_rmsnorm_q8(const void* x, int dtype, int64_t ldx, const void* residual, int64_t ldr, const void* gain,
+                      int gain_dtype, int M, int d, float eps, void* h_out, int64_t ldh, int8_t* q, int64_t ldq,
+                      float* scale, void* stream) {
+  const size_t es = dtype_bytes(dtype);
+  if (!es) return einval("dspark_rmsnorm_q8: dtype must be DSPARK_F32, DSPARK_BF16 or DSPARK_F16");
+  if (gain_dtype != dtype && gain_dtype != DSPARK_F32) return einval("dspark_rmsnorm_q8: gain_dtype must be dtype or DSPARK_F32");
+  if (M < 0 || d < 1) return einval("dspark_rmsnorm_q8: M must be >= 0 and d >= 1");
+  if (ldx < d || ldq < d || (residual && (ldr < d || ldh < d)))
+    return einval("dspark_rmsnorm_q8: row strides must be >= d");
+  if (!(eps > 0.f) || std::isinf(eps)) return einval("dspark_rmsnorm_q8: eps must be finite and > 0");
+  if (M == 0) return DSPARK_OK;
+  if (!x || !q || !scale || (residual && !h_out)) return einval("dspark_rmsnorm_q8: null pointer");
+  if ((uintptr_t)x % es || (uintptr_t)residual % es || (residual && (uintptr_t)h_out % es) ||
+      (uintptr_t)gain % dtype_bytes(gain_dtype))
+    return einval("dspark_rmsnorm_q8: tensors must be aligned to their type");
+  if (residual) {
+    if (bad_overlap(h_out, ldh, x, ldx, M, d, es) || bad_overlap(h_out, ldh, residual, ldr, M, d, es))
+      return einval("dspark_rmsnorm_q8: h_out overlaps an input without being it");
+  }
+  NormQ8Call c{x, dtype, ldx, residual, ldr, gain, gain_dtype == DSPARK_F32, M, d, 1, eps, residual ? h_out : nullptr, ldh, q,
+               ldq, scale, (cudaStream_t)stream};
+  return launch_norm_q8(c);
+}
+
+int dspark_quantize_q8(const void* x, int dtype, int64_t ldx, int M, int d, int8_t* q, int64_t ldq, float* scale,
+                       void* stream) {
+  const size_t es = dtype_bytes(dtype);
+  if (!es) return einval("dspark_quantize_q8: dtype must be DSPARK_F32, DSPARK_BF16 or DSPARK_F16");
+  if (M < 0 || d < 1) return einval("dspark_quantize_q8: M must be >= 0 and d >= 1");
+  if (ldx < d || ldq < d) return einval("dspark_quantize_q8: row strides must be >= d");
+  if (M == 0) return DSPARK_OK;
+  if (!x || !q || !scale) return einval("dspark_quantize_q8: null pointer");
+  if ((uintptr_t)x % es) return einval("dspark_quantize_q8: x must be aligned to its type");
+  NormQ8Call c{x, dtype, ldx, nullptr, 0, nullptr, 1, M, d, 0, 0.f, nullptr, 0, q, ldq, scale, (cudaStream_t)stream};
+  return launch_norm_q8(c);
+}
+
+int dspark_matmul_q8(const int8_t* q, int64_t ldq, const float* q_scale, const int8_t* w, int64_t ldw,
+                     const float* w_scale, int M, int N, int K, void* out, int out_dtype, int64_t ldo, uint32_t* flags,
+                     void* stream) {
+  const size_t es = dtype_bytes(out_dtype);
+  if (!es) return einval("dspark_matmul_q8: out_dtype must be DSPARK_F32, DSPARK_BF16 or DSPARK_F16");
+  if (M < 0 || N < 1 || K < 1) return einval("dspark_matmul_q8: M must be >= 0, N and K >= 1");
+  if (K > kMaxMatmulQ8K) return einval("dspark_matmul_q8: K must be <= 131071");
+  if (ldq < K || ldw < K || ldo < N) return einval("dspark_matmul_q8: row strides must not be below the row length");
+  if (ldq % 16 || ldw % 16) return einval("dspark_matmul_q8: ldq and ldw must be multiples of 16");
+  if (ldq >= (1ll << 40) || ldw >= (1ll << 40)) return einval("dspark_matmul_q8: row stride too large");
+  if (M == 0) return DSPARK_OK;
+  if (!q || !q_scale || !w || !w_scale || !out) return einval("dspark_matmul_q8: null pointer");
+  if ((uintptr_t)q % 16 || (uintptr_t)w % 16) return einval("dspark_matmul_q8: q and w must be 16-byte aligned");
+  if ((uintptr_t)out % es) return einval("dspark_matmul_q8: out must be aligned to its type");
+  if ((long long)(M / 16 + 1) * (N / 16 + 1) >= (1ll << 31)) return einval("dspark_matmul_q8: product too large");
+  MatmulQ8Call c{q, ldq, q_scale, w, ldw, w_scale, M, N, K, out, out_dtype, ldo, flags, (cudaStream_t)stream};
+  return launch_matmul_q8(c);
 }
 
 }  // extern "C"

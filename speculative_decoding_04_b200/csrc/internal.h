@@ -1,6 +1,7 @@
 // Host-side interface between the C ABI (api.cu) and the kernel launchers.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
@@ -172,6 +173,46 @@ struct LogprobsBwdCall {
   cudaStream_t stream;
 };
 dspark_status launch_token_logprobs_backward(const LogprobsBwdCall& c);
+
+struct NormQ8Call {
+  const void* x;
+  int dtype;
+  long long ldx;
+  const void* residual;
+  long long ldr;
+  const void* gain;
+  int gain_f32;
+  int M, d, norm;
+  float eps;
+  void* h;
+  long long ldh;
+  int8_t* q;
+  long long ldq;
+  float* scale;
+  cudaStream_t stream;
+};
+dspark_status launch_norm_q8(const NormQ8Call& c);
+
+struct MatmulQ8Call {
+  const int8_t* q;
+  long long ldq;
+  const float* q_scale;
+  const int8_t* w;
+  long long ldw;
+  const float* w_scale;
+  int M, N, K;
+  void* out;
+  int out_dtype;
+  long long ldo;
+  uint32_t* flags;
+  cudaStream_t stream;
+};
+dspark_status launch_matmul_q8(const MatmulQ8Call& c);
+constexpr int kMaxMatmulQ8K = 131071;  // |sum| < 2^31 for any 8-bit values
+
+// A 2-D tensor map of bytes, innermost dimension first, in boxes of 128-byte swizzled rows.
+bool encode_tensor_map_u8(CUtensorMap* m, void* base, const uint64_t* dims, const uint64_t* strides_bytes,
+                          const uint32_t* box);
 
 size_t draft_workspace_bytes(int B, int gamma, int V, int r);
 size_t rnn_draft_workspace_bytes(int B, int gamma, int V, int r);

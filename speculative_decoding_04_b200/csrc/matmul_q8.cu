@@ -1,0 +1,298 @@
+// Integer matrix product with scales: out[m, n] = q_scale[m] * w_scale[n] * sum_k q[m, k] w[n, k].
+//
+// The product is computed transposed on the tensor cores (tcgen05.mma kind::i8, int32 accumulators in
+// tensor memory): the weights' rows n are the MMA's M dimension (the 128 TMEM lanes) and the tokens m
+// its N dimension (TMEM columns), so that a few tokens waste no MMA rows and a warp's store covers 32
+// consecutive outputs of one token.  Both operands are K-major as they lie in memory: TMA boxes of 128
+// bytes of K (128-byte swizzle) by BV weight rows or BN tokens; K and rows past the end read as zero.
+//   warp 0      TMA producer, a ring of stages [BV x 128 B of weights | BN x 128 B of tokens]
+//   warp 1      MMA issuer: per stage 4 steps of K = 32, for one or two blocks of 128 weight rows
+//   warp 2      TMEM allocation
+//   warps 4-11  epilogue: TMEM -> registers, the two scales, stores
+// Persistent: one CTA per SM takes tiles in turn, the token tiles of one weight tile next to each
+// other, so that a weight tile comes from HBM once.
+//
+// The sum is exact (int32: K <= 131071 keeps |sum| below 2^31 even for -128 * -128); it is rounded to
+// fp32 once, multiplied by the two scales in fp32 and rounded once to the output's type.
+
+#include <cudaTypedefs.h>
+#include <cuda_fp16.h>
+
+#include <algorithm>
+#include <string>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace dspark {
+
+namespace {
+
+constexpr int kMqThreads = 384;
+constexpr int kMqEpiWarps = 8;
+constexpr int kMqKB = 128;  // bytes (= values) of K per stage
+constexpr int kMqMaxStages = 8;
+constexpr uint32_t kMqSmem = 227u * 1024u;
+
+struct MqArgs {
+  const float* q_scale;
+  const float* w_scale;
+  void* out;
+  long long ldo;
+  uint32_t* flags;
+  int M, N, K;
+  int bv, bn;          // tile: weight rows (multiple of 16, <= 256), tokens (multiple of 16, <= 256)
+  int ntok, ntiles;    // token tiles; tiles in all
+  int stages, nbuf, blocks, tmem_cols;
+  uint32_t w_bytes, stage_bytes, bars;  // offsets within the aligned shared memory
+};
+
+struct MqSync {
+  volatile int* abort;
+};
+
+// Bounded wait shared by all roles; after any timeout every later wait returns at once.
+__device__ __forceinline__ bool mq_wait(const MqSync& s, uint64_t* bar, uint32_t parity) {
+  if (*s.abort) return false;
+  for (uint32_t i = 0; i < kSpinLimit; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 1023u) == 1023u && *s.abort) return false;
+  }
+  *s.abort = 1;
+  return false;
+}
+
+__device__ __forceinline__ void tc_mma_i8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// 32 lanes x 16 consecutive 32-bit columns (no wait).
+__device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
+template <int DT>
+__device__ __forceinline__ void store_out(void* out, long long i, float v) {
+  if (DT == DSPARK_F32) static_cast<float*>(out)[i] = v;
+  else if (DT == DSPARK_BF16) static_cast<__nv_bfloat16*>(out)[i] = __float2bfloat16_rn(v);
+  else static_cast<__half*>(out)[i] = __float2half_rn(v);
+}
+
+template <int DT>
+__global__ void __launch_bounds__(kMqThreads, 1)
+    matmul_q8_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, MqArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint64_t* full = reinterpret_cast<uint64_t*>(sm + a.bars);
+  uint64_t* empty = full + kMqMaxStages;
+  uint64_t* t_full = empty + kMqMaxStages;
+  uint64_t* t_empty = t_full + 2;
+  uint64_t* drain = t_empty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const MqSync sy{s_abort};
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int nkb = (a.K + kMqKB - 1) / kMqKB;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < a.stages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&t_full[i], 1);
+      mbar_init(&t_empty[i], kMqEpiWarps);
+    }
+    mbar_init(drain, 1);
+    *s_abort = 0;
+    fence_mbar_init();
+    prefetch_tmap(&tmW);
+    prefetch_tmap(&tmX);
+  }
+  if (warp == 2) {
+    tmem_alloc(tmem_slot, a.tmem_cols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int it = 0;
+      bool ok = true;
+      for (int t = blockIdx.x; ok && t < a.ntiles; t += gridDim.x) {
+        const int v0 = (t / a.ntok) * a.bv, m0 = (t % a.ntok) * a.bn;
+        for (int k = 0; k < nkb; ++k, ++it) {
+          const int s = it % a.stages;
+          if (!mq_wait(sy, &empty[s], ((it / a.stages) & 1) ^ 1)) {
+            ok = false;
+            break;
+          }
+          uint8_t* st = sm + s * a.stage_bytes;
+          mbar_arrive_expect_tx(&full[s], (uint32_t)(a.bv + a.bn) * kMqKB);
+          tma_load_2d(st, &tmW, k * kMqKB, v0, &full[s]);
+          tma_load_2d(st + a.w_bytes, &tmX, k * kMqKB, m0, &full[s]);
+        }
+      }
+      if (*s_abort)  // let the copies already issued land (bounded) before the CTA exits
+        for (int i = max(0, it - a.stages); i < it; ++i)
+          for (uint32_t n = 0; n < kSpinLimit && !mbar_try_wait(&full[i % a.stages], (i / a.stages) & 1); ++n) {
+          }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      const uint32_t idesc = (2u << 4)                          // D int32
+                             | (1u << 7) | (1u << 10)           // A, B signed 8-bit
+                             | ((uint32_t)(a.bn >> 3) << 17)    // N
+                             | ((uint32_t)(128 >> 4) << 24);    // M
+      int it = 0, n = 0;
+      bool ok = true;
+      for (int t = blockIdx.x; ok && t < a.ntiles; t += gridDim.x, ++n) {
+        const int buf = n % a.nbuf;
+        if (!mq_wait(sy, &t_empty[buf], ((n / a.nbuf) & 1) ^ 1)) break;
+        tc_fence_after();
+        const uint32_t acc = tmem + (uint32_t)(buf * a.blocks * a.bn);
+        for (int k = 0; k < nkb; ++k, ++it) {
+          const int s = it % a.stages;
+          if (!mq_wait(sy, &full[s], (it / a.stages) & 1)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t w = smem_u32(sm + s * a.stage_bytes), x = w + a.w_bytes;
+          for (int b = 0; b < a.blocks; ++b)
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              tc_mma_i8(acc + (uint32_t)(b * a.bn), smem_desc(w + b * 16384u + kk * 32u, 16u, 1024u, 2u),
+                        smem_desc(x + kk * 32u, 16u, 1024u, 2u), idesc, (k | kk) != 0 ? 1u : 0u);
+          tc_commit(&empty[s]);
+        }
+        if (ok) tc_commit(&t_full[buf]);
+      }
+      if (*s_abort) {  // tensor memory and the stages stay until the MMAs already issued are done (bounded)
+        tc_commit(drain);
+        mbar_wait(drain, 0);
+      }
+    }
+  } else if (warp >= 4) {
+    const int q = warp & 3, b = (warp - 4) >> 2;
+    int n = 0;
+    for (int t = blockIdx.x; t < a.ntiles; t += gridDim.x, ++n) {
+      const int buf = n % a.nbuf;
+      const int v = (t / a.ntok) * a.bv + b * 128 + q * 32 + lane, m0 = (t % a.ntok) * a.bn;
+      const bool mine = b < a.blocks && b * 128 + q * 32 + lane < a.bv && v < a.N;
+      const float sw = mine ? __ldg(a.w_scale + v) : 0.f;
+      const int nm = min(a.bn, a.M - m0);
+      const bool ok = __all_sync(0xffffffffu, mq_wait(sy, &t_full[buf], (n / a.nbuf) & 1));
+      tc_fence_after();
+      if (b < a.blocks) {
+        const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)((buf * a.blocks + b) * a.bn);
+        for (int c = 0; c < nm; c += 16) {
+          uint32_t r[16];
+          if (ok) {
+            tmem_ld_x16(acc + c, r);
+            tmem_wait_ld();
+          }
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            if (c + j < nm && mine) {
+              const int m = m0 + c + j;
+              const float o = ok ? (float)(int32_t)r[j] * __ldg(a.q_scale + m) * sw : __int_as_float(0x7FC00000);
+              store_out<DT>(a.out, (long long)m * a.ldo + v, o);
+            }
+        }
+        if (!ok && a.flags && q == 0 && b == 0)
+          for (int m = m0 + lane; m < m0 + nm; m += 32) atomicOr(a.flags + m, DSPARK_FLAG_DEVICE_TIMEOUT);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&t_empty[buf]);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 2) tmem_dealloc(tmem, a.tmem_cols);
+}
+
+template <int DT>
+static cudaError_t launch_mq(const CUtensorMap& mW, const CUtensorMap& mX, const MqArgs& a, int grid, size_t smem,
+                             cudaStream_t st) {
+  auto kern = matmul_q8_kernel<DT>;
+  cudaError_t rc = ensure_smem_attr((const void*)kern, smem);
+  if (rc != cudaSuccess) return rc;
+  kern<<<grid, kMqThreads, smem, st>>>(mW, mX, a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+dspark_status launch_matmul_q8(const MatmulQ8Call& c) {
+  if (c.M == 0) return DSPARK_OK;
+  const int sms = device_sm_count();
+  MqArgs a{};
+  a.q_scale = c.q_scale;
+  a.w_scale = c.w_scale;
+  a.out = c.out;
+  a.ldo = c.ldo;
+  a.flags = c.flags;
+  a.M = c.M;
+  a.N = c.N;
+  a.K = c.K;
+  a.ntok = (c.M + 255) / 256;
+  a.bn = ((c.M + a.ntok - 1) / a.ntok + 15) / 16 * 16;
+  // weight rows per tile: the largest tile that gives every CTA the same number of tiles
+  const int per = std::max(1, (int)(((long long)c.N * a.ntok + 256ll * sms - 1) / (256ll * sms)));
+  long long rows = ((long long)c.N * a.ntok + (long long)sms * per - 1) / ((long long)sms * per);
+  a.bv = (int)std::min(256ll, std::max(16ll, (rows + 15) / 16 * 16));
+  a.ntiles = a.ntok * ((c.N + a.bv - 1) / a.bv);
+  a.blocks = a.bv > 128 ? 2 : 1;
+  a.nbuf = 2 * a.blocks * a.bn <= 512 ? 2 : 1;
+  a.tmem_cols = 32;
+  while (a.tmem_cols < a.nbuf * a.blocks * a.bn) a.tmem_cols *= 2;
+  a.w_bytes = (uint32_t)(a.bv * kMqKB + 1023) / 1024 * 1024;
+  a.stage_bytes = a.w_bytes + (uint32_t)(a.bn * kMqKB + 1023) / 1024 * 1024;
+  // an MMA reads 128 weight rows whatever the tile holds: what follows the last stage is readable
+  const uint32_t slack = (uint32_t)(a.blocks * 16384) > a.stage_bytes ? a.blocks * 16384 - a.stage_bytes : 0;
+  const uint32_t misc = 8 * (2 * kMqMaxStages + 5) + 16;
+  a.stages = (int)std::min<uint32_t>(kMqMaxStages, (kMqSmem - 1024 - misc - slack) / a.stage_bytes);
+  a.bars = a.stages * a.stage_bytes + slack;
+  const size_t smem = 1024 + a.bars + misc;
+  CUtensorMap mW, mX;
+  const uint64_t wd[2] = {(uint64_t)c.K, (uint64_t)c.N}, xd[2] = {(uint64_t)c.K, (uint64_t)c.M};
+  const uint64_t ws[1] = {(uint64_t)c.ldw}, xs[1] = {(uint64_t)c.ldq};
+  const uint32_t wb[2] = {(uint32_t)kMqKB, (uint32_t)a.bv}, xb[2] = {(uint32_t)kMqKB, (uint32_t)a.bn};
+  if (!encode_tensor_map_u8(&mW, const_cast<int8_t*>(c.w), wd, ws, wb) ||
+      !encode_tensor_map_u8(&mX, const_cast<int8_t*>(c.q), xd, xs, xb)) {
+    set_error("dspark_matmul_q8: cuTensorMapEncodeTiled failed");
+    return DSPARK_ECUDA;
+  }
+  const int grid = std::min(sms, a.ntiles);
+  cudaError_t rc;
+  switch (c.out_dtype) {
+    case DSPARK_F32: rc = launch_mq<DSPARK_F32>(mW, mX, a, grid, smem, c.stream); break;
+    case DSPARK_BF16: rc = launch_mq<DSPARK_BF16>(mW, mX, a, grid, smem, c.stream); break;
+    default: rc = launch_mq<DSPARK_F16>(mW, mX, a, grid, smem, c.stream); break;
+  }
+  if (rc != cudaSuccess) {
+    set_error(std::string("matmul_q8 launch: ") + cudaGetErrorString(rc));
+    return DSPARK_ECUDA;
+  }
+  return DSPARK_OK;
+}
+
+}  // namespace dspark

@@ -100,6 +100,12 @@ def _load() -> ctypes.CDLL:
     lib.dspark_token_logprobs_backward.restype = _i
     lib.dspark_token_logprobs_backward.argtypes = [_vp, _i, _i64, _vp, _i, _i, _f, _vp, _vp, _vp, _vp, _i, _vp, _vp,
                                                    _vp, _i64, _vp]
+    lib.dspark_rmsnorm_q8.restype = _i
+    lib.dspark_rmsnorm_q8.argtypes = [_vp, _i, _i64, _vp, _i64, _vp, _i, _i, _i, _f, _vp, _i64, _vp, _i64, _vp, _vp]
+    lib.dspark_quantize_q8.restype = _i
+    lib.dspark_quantize_q8.argtypes = [_vp, _i, _i64, _i, _i, _vp, _i64, _vp, _vp]
+    lib.dspark_matmul_q8.restype = _i
+    lib.dspark_matmul_q8.argtypes = [_vp, _i64, _vp, _vp, _i64, _vp, _i, _i, _i, _vp, _i, _i64, _vp, _vp]
     return lib
 
 
@@ -464,14 +470,14 @@ def prefix_schedule_t2(c: torch.Tensor, sps: torch.Tensor, D_max: int, ring: tor
     return L_out, a_out, theta_out, K_out, flags
 
 
-def _rows2d(t: torch.Tensor, name: str) -> torch.Tensor:
+def _rows2d(t: torch.Tensor, name: str, dtypes=_DTYPES) -> torch.Tensor:
     """t as [rows, columns] without a copy: columns dense, rows a constant stride apart."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype not in _DTYPES:
-        raise ValueError(f"{name} must be fp32, bf16 or fp16, got {t.dtype}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
     if t.dim() < 2:
         raise ValueError(f"{name} must have at least 2 dimensions")
     if t.dim() > 2:
@@ -598,3 +604,105 @@ def token_logprobs_backward(logits: torch.Tensor, tokens: torch.Tensor, T: float
         g2.data_ptr(), _ld(g2), torch.cuda.current_stream().cuda_stream)
     _check("dspark_token_logprobs_backward", st)
     return grad
+
+
+def _q8_rows(lead, d: int, dev) -> torch.Tensor:
+    """An int8 tensor [*lead, d] whose rows start on 16 bytes (what matmul_q8 reads)."""
+    ld = (d + 15) // 16 * 16
+    q = torch.empty(tuple(lead) + (ld,), dtype=torch.int8, device=dev)
+    return q if ld == d else q[..., :d]
+
+
+def _like(t: torch.Tensor, name: str, ref: torch.Tensor, dtype) -> torch.Tensor:
+    """t as rows, after checking that it has ref's shape and device and the given dtype."""
+    t2 = _rows2d(t, name, (dtype,))
+    if t.shape != ref.shape or t.device != ref.device:
+        raise ValueError(f"{name} must be {tuple(ref.shape)} on {ref.device}, got {tuple(t.shape)} on {t.device}")
+    return t2
+
+
+def rmsnorm_q8(x: torch.Tensor, gain: Optional[torch.Tensor], eps: float, *, residual: Optional[torch.Tensor] = None,
+               h_out=None, q=None, scale=None, stream=None):
+    """Root-mean-square norm of the rows of x (+ residual), as int8 with one scale per row.
+
+    x, residual [..., d] (fp32, bf16 or fp16; rows a constant stride apart), gain [d] (x's dtype, fp32,
+    or None).  Returns (q [..., d] int8 with rows on 16 bytes, scale [...] fp32, h = x + residual in
+    x's dtype, or None without a residual): q * scale is the normalised row.  h_out may be x or the
+    residual."""
+    x2 = _rows2d(x, "x")
+    dev = x2.device
+    if _elsewhere(dev, stream):
+        return _at(rmsnorm_q8, dev, stream, x, gain, eps, residual=residual, h_out=h_out, q=q, scale=scale)
+    M, d = x2.shape
+    gdt = x2.dtype
+    if gain is not None and gain.dtype != gdt:
+        gdt = torch.float32
+    r2 = h2 = None
+    if residual is not None:
+        r2 = _like(residual, "residual", x, x.dtype)
+        h_out = torch.empty(x.shape, dtype=x.dtype, device=dev) if h_out is None else h_out
+        h2 = _like(h_out, "h_out", x, x.dtype)
+    else:
+        h_out = None
+    q = _q8_rows(x.shape[:-1], d, dev) if q is None else q
+    q2 = _like(q, "q", x, torch.int8)
+    scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev) if scale is None else scale
+    st = lib.dspark_rmsnorm_q8(
+        x2.data_ptr(), _DTYPES[x2.dtype], _ld(x2), None if r2 is None else r2.data_ptr(), 0 if r2 is None else _ld(r2),
+        _arg(gain, "gain", gdt, d, dev), _DTYPES[gdt], M, d, float(eps), None if h2 is None else h2.data_ptr(),
+        0 if h2 is None else _ld(h2), q2.data_ptr(), _ld(q2), _arg(scale, "scale", torch.float32, M, dev),
+        torch.cuda.current_stream().cuda_stream)
+    _check("dspark_rmsnorm_q8", st)
+    return q, scale, h_out
+
+
+def quantize_q8(x: torch.Tensor, *, q=None, scale=None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """The rows of x [..., d] as int8 with one scale per row: (q, scale), x about q * scale."""
+    x2 = _rows2d(x, "x")
+    dev = x2.device
+    if _elsewhere(dev, stream):
+        return _at(quantize_q8, dev, stream, x, q=q, scale=scale)
+    M, d = x2.shape
+    q = _q8_rows(x.shape[:-1], d, dev) if q is None else q
+    q2 = _like(q, "q", x, torch.int8)
+    scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev) if scale is None else scale
+    st = lib.dspark_quantize_q8(x2.data_ptr(), _DTYPES[x2.dtype], _ld(x2), M, d, q2.data_ptr(), _ld(q2),
+                                _arg(scale, "scale", torch.float32, M, dev), torch.cuda.current_stream().cuda_stream)
+    _check("dspark_quantize_q8", st)
+    return q, scale
+
+
+def matmul_q8(q: torch.Tensor, q_scale: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor, *,
+              out_dtype=torch.float32, out=None, flags=None, stream=None) -> torch.Tensor:
+    """out[..., n] = q_scale[...] * w_scale[n] * sum_k q[..., k] w[n, k]: the LM head on int8 weights.
+
+    q [..., K] and w [N, K] int8 with rows on 16 bytes (as rmsnorm_q8 and quantize_q8 make them), the
+    scales fp32 with one value per row.  out: [..., N] in out_dtype (fp32, bf16 or fp16), or None: a new
+    tensor.  With q in the order of U or l_t an fp32 result feeds markov_draft or verify."""
+    q2 = _rows2d(q, "q", (torch.int8,))
+    dev = q2.device
+    if _elsewhere(dev, stream):
+        return _at(matmul_q8, dev, stream, q, q_scale, w, w_scale, out_dtype=out_dtype, out=out, flags=flags)
+    w2 = _rows2d(w, "w", (torch.int8,))
+    if w.dim() != 2 or w.device != dev:
+        raise ValueError(f"w must be [N, K] on {dev}")
+    M, K = q2.shape
+    N = w2.shape[0]
+    if w2.shape[1] != K:
+        raise ValueError(f"q has rows of {K}, w of {w2.shape[1]}")
+    if out is None:
+        if out_dtype not in _DTYPES:
+            raise ValueError(f"out_dtype must be fp32, bf16 or fp16, got {out_dtype}")
+        out = torch.empty(q.shape[:-1] + (N,), dtype=out_dtype, device=dev)
+        o2 = out.view(-1, N) if out.dim() != 2 else out
+    else:
+        o2 = _rows2d(out, "out")
+        if out.device != dev or out.shape != q.shape[:-1] + (N,):
+            raise ValueError(f"out must be {tuple(q.shape[:-1]) + (N,)} on {dev}, got {tuple(out.shape)}")
+    ldq, ldw = (t.stride(0) if t.shape[0] > 1 else (K + 15) // 16 * 16 for t in (q2, w2))
+    st = lib.dspark_matmul_q8(
+        q2.data_ptr(), ldq, _arg(q_scale, "q_scale", torch.float32, M, dev), w2.data_ptr(), ldw,
+        _arg(w_scale, "w_scale", torch.float32, N, dev), M, N, K, o2.data_ptr(), _DTYPES[o2.dtype], _ld(o2),
+        _arg(flags, "flags", torch.int32, M, dev), torch.cuda.current_stream().cuda_stream)
+    _check("dspark_matmul_q8", st)
+    return out

@@ -59,3 +59,31 @@ def test_logprobs_gradient_by_differences():
         e[i] = 1e-5
         num[i] = (f(l + e) - f(l - e)) / 2e-5
     assert np.allclose(g, num, atol=1e-8) and np.all(g[2] == 0)
+
+
+def test_quantisation_closed_forms():
+    x = np.array([[127.0, -63.5, 1.0, 0.0], [0.0, 0.0, 0.0, 0.0], [1.0, np.inf, 0, 0], [np.nan, 1, 2, 3]])
+    q, s = O.quantize_q8(x)
+    assert q[0].tolist() == [127, -64, 1, 0] and s[0] == 1.0      # -63.5 rounds to even
+    assert not q[1:].any() and s[1] == 0 and np.isnan(s[2:]).all()
+    h = np.array([[3.0, -4.0]])                                   # root mean square 5 / sqrt(2)
+    q, s = O.rmsnorm_q8(h, np.array([1.0, 0.5]), 0.0)
+    assert q[0].tolist() == [127, -85]                            # v = (3, -2)
+    assert np.isclose(s[0], 3 / (5 / np.sqrt(2)) / 127)
+
+
+def test_quantisation_error_is_half_a_step():
+    rng = np.random.default_rng(3)
+    h, g = rng.normal(size=(20, 300)), 1 + 0.1 * rng.normal(size=300)
+    q, s = O.rmsnorm_q8(h, g, 1e-6)
+    h32, g32 = h.astype(np.float32).astype(np.float64), g.astype(np.float32).astype(np.float64)
+    y = h32 * g32 / np.sqrt((h32 ** 2).mean(1, keepdims=True) + 1e-6)
+    assert np.all(np.abs(q * s[:, None] - y) <= s[:, None] * (0.5 + 1e-4)) and np.abs(q).max() == 127
+
+
+def test_matmul_q8_against_integers():
+    rng = np.random.default_rng(4)
+    q, w = rng.integers(-128, 128, (5, 64)), rng.integers(-128, 128, (7, 64))
+    a, b = rng.random(5), rng.random(7)
+    want = [[a[i] * b[j] * sum(int(x) * int(y) for x, y in zip(q[i], w[j])) for j in range(7)] for i in range(5)]
+    assert np.allclose(O.matmul_q8(q, a, w, b), want, rtol=1e-15)
