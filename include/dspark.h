@@ -436,7 +436,7 @@ int dspark_prefix_schedule_t2(const float* c, const double* sps, int B, int gamm
  *          (required when top > 0).  stats [N, 2] fp32 or NULL, 8-byte aligned.
  * flags    [N] uint32 or NULL, OR'ed with NONFINITE / TOKEN_RANGE / RAGGED_OFFSETS of each entry.
  * Sums are fp32 per lane, joined in fp64; results do not depend on timing.  N = 0 does nothing.
- * Limits: V <= 2^24, N <= 2^26.  No workspace.
+ * Limits: V <= 2^21, N <= 2^26.  No workspace.
  * -------------------------------------------------------------------------- */
 #define DSPARK_TOP_MAX 32
 int dspark_token_logprobs(const void* logits, int dtype, int64_t ld, int64_t n_rows, const int64_t* rows,

@@ -325,7 +325,7 @@ int dspark_token_logprobs(const void* logits, int dtype, int64_t ld, int64_t n_r
   const size_t es = dtype_bytes(dtype);
   if (!es) return einval("dspark_token_logprobs: dtype must be DSPARK_F32, DSPARK_BF16 or DSPARK_F16");
   if (N < 0 || V < 1) return einval("dspark_token_logprobs: N must be >= 0 and V >= 1");
-  if (V > kMaxLogprobsV) return einval("dspark_token_logprobs: V must be <= 2^24");
+  if (V > kMaxLogprobsV) return einval("dspark_token_logprobs: V must be <= 2^21");
   if (ld < V) return einval("dspark_token_logprobs: ld must be >= V");
   if (n_rows < 0 || (!rows && n_rows < N)) return einval("dspark_token_logprobs: fewer rows than entries");
   if (n_rows > 0 && ld > INT64_MAX / 8 / n_rows) return einval("dspark_token_logprobs: tensor too large");
@@ -349,7 +349,7 @@ int dspark_token_logprobs_backward(const void* logits, int dtype, int64_t ld, co
   const size_t es = dtype_bytes(dtype);
   if (!es) return einval("dspark_token_logprobs_backward: dtype must be DSPARK_F32, DSPARK_BF16 or DSPARK_F16");
   if (N < 0 || V < 1) return einval("dspark_token_logprobs_backward: N must be >= 0 and V >= 1");
-  if (V > kMaxLogprobsV) return einval("dspark_token_logprobs_backward: V must be <= 2^24");
+  if (V > kMaxLogprobsV) return einval("dspark_token_logprobs_backward: V must be <= 2^21");
   if (ld < V || ldg < V) return einval("dspark_token_logprobs_backward: ld and ldg must be >= V");
   if (N > 0 && (ld > INT64_MAX / 8 / N || ldg > INT64_MAX / 8 / N))
     return einval("dspark_token_logprobs_backward: tensor too large");

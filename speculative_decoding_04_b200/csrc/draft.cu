@@ -1256,11 +1256,6 @@ static bool make_map(CUtensorMap* m, CUtensorMapDataType dt, int rank, void* bas
   return rc == CUDA_SUCCESS;
 }
 
-bool encode_tensor_map_u8(CUtensorMap* m, void* base, const uint64_t* dims, const uint64_t* strides_bytes,
-                          const uint32_t* box) {
-  return make_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, base, dims, strides_bytes, box);
-}
-
 template <typename K, typename... Args>
 static cudaError_t launch_ex(K kernel, dim3 grid, dim3 block, size_t smem, cudaStream_t st, bool pdl, bool coop,
                              Args... args) {

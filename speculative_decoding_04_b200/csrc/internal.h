@@ -1,7 +1,6 @@
 // Host-side interface between the C ABI (api.cu) and the kernel launchers.
 #pragma once
 
-#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
@@ -210,10 +209,6 @@ struct MatmulQ8Call {
 dspark_status launch_matmul_q8(const MatmulQ8Call& c);
 constexpr int kMaxMatmulQ8K = 131071;  // |sum| < 2^31 for any 8-bit values
 
-// A 2-D tensor map of bytes, innermost dimension first, in boxes of 128-byte swizzled rows.
-bool encode_tensor_map_u8(CUtensorMap* m, void* base, const uint64_t* dims, const uint64_t* strides_bytes,
-                          const uint32_t* box);
-
 size_t draft_workspace_bytes(int B, int gamma, int V, int r);
 size_t rnn_draft_workspace_bytes(int B, int gamma, int V, int r);
 size_t verify_workspace_bytes(int B, int gamma, int V);
@@ -229,7 +224,7 @@ dspark_status launch_schedule(const ScheduleCall& c);
 
 constexpr int kMaxGamma = 64;
 constexpr int kMaxScheduleItems = 16384;
-constexpr int kMaxLogprobsV = 1 << 24;  // tiles of 2 KB, at most 4096 of them for each of 16 CTAs
+constexpr int kMaxLogprobsV = 1 << 21;  // 4096 tiles of 2 KB (fp32) whose maxima a CTA holds
 constexpr int kMaxLogprobsN = 1 << 26;  // 16 CTAs each
 constexpr size_t kWsHeader = 256;
 

@@ -6,17 +6,25 @@
 // Both terms of H are non-negative, so nothing cancels.
 //
 // Forward.  One cluster of C CTAs per row (C = 1 when the rows alone fill the GPU), the row cut into
-// tiles of 2 KB that are contiguous in the vocabulary; the warps of a CTA take its tiles in turn.  One
-// pass: a warp loads a tile (four 16-byte loads a lane, the next tile's loads in flight meanwhile),
-// reduces its maximum, keeps it in shared memory as the tile's record and adds the tile to the warp's
-// running (R, S, E) = (reference, sum 2^x, sum 2^x x), x = (l - R) log2(e)/T, rescaled when R grows.
-// The sums are fp32 per lane (some 300 terms), joined over warps and CTAs in fp64.
+// tiles of 512 values that are contiguous in the vocabulary; the warps of a CTA take its tiles in turn.
+// One pass: a warp loads a tile (two or four 16-byte loads a lane, the next tile's loads in flight
+// meanwhile), reduces its maximum, keeps it in shared memory as the tile's record and adds the tile to
+// the warp's running (R, S, E) = (reference, sum 2^x, sum 2^x x), x = (l - R) log2(e)/T, rescaled when R
+// grows.  The sums are fp32 per lane (some 300 terms), joined pairwise over lanes, warps and CTAs; the
+// logarithm and what follows are fp64.
+// The loop costs about 6 instructions a value (packed fp32 pairs; one ex2), which at 16 bits a value is
+// near what the SM can issue while HBM streams: 1088 x 151936 fp32 takes 119 us (5.5 TB/s), 2048 x 262144
+// bf16 192 us.  CTAs of 8 warps, four to an SM, hide each other's row ends better than two of 16 (131
+// against 141 us); a ring filled by 16-byte asynchronous copies measured 139 us (its shared-memory
+// traffic competes with the exponentials), two or three tiles ahead 133 and 143 (fewer warps fit), and
+// rows' values clamped one by one against -inf 204 us in bf16 (hence the two forms of the loop).
 //
 // Alternatives.  The main pass spends nothing on them beyond the tiles' maxima.  The k best elements
 // (value descending, index ascending) lie in the k best tiles ordered by (maximum descending, tile
 // ascending): an element outside them is beaten by each of those tiles' maxima, on a tie by its lower
-// index, because a tile is a contiguous range.  So the k tiles are read again (from L2), each yields
-// at most k candidates at or above the k-th tile's maximum, and the candidates are ranked by counting.
+// index, because a tile is a contiguous range.  So the k tiles are read again (from L2, spread over the
+// cluster), each yields at most k candidates at or above the k-th tile's maximum, and the candidates
+// are ranked by counting.
 //
 // Backward.  One pass over the row: with G = g_logp + sum_j g_top,j and p, log p from (m, ln S),
 //   dl = ( g_logp 1_tok + sum_j g_top,j 1_idx_j - p (G + g_H (log p + H)) ) / T,
@@ -38,13 +46,8 @@ namespace dspark {
 
 namespace {
 
-constexpr int kLpWarps = 16;
-constexpr int kLpThreads = kLpWarps * 32;
-constexpr int kLpMaxTiles = 4096;   // tiles of one CTA (2 KB each): 16 KB of maxima
 constexpr int kLpMaxCluster = 16;
-constexpr int kLpCand = DSPARK_TOP_MAX * DSPARK_TOP_MAX;
 
-constexpr double kLog2eD = 1.4426950408889634074;
 constexpr double kLn2D = 0.69314718055994530942;
 
 struct LpArgs {
@@ -101,11 +104,6 @@ struct Elem<DSPARK_F16> {
   }
 };
 
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float d;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
-  return d;
-}
 // max of three, NaN if any is (sm_100)
 __device__ __forceinline__ float max3_nan(float a, float b, float c) {
   float d;
@@ -141,7 +139,8 @@ template <int DT>
 struct RowTiles {
   using E = Elem<DT>;
   using T = typename E::T;
-  static constexpr int kTile = 32 * 4 * E::kVec;
+  static constexpr int kLoads = sizeof(T);  // 16-byte vectors of a tile a lane holds
+  static constexpr int kTile = 32 * kLoads * E::kVec;
   const T* p;
   int V, head, n;
   __device__ RowTiles(const T* p_, int V_) : p(p_), V(V_) {
@@ -151,21 +150,23 @@ struct RowTiles {
   }
   __device__ int start(int t) const { return head > 0 ? (t == 0 ? 0 : head + (t - 1) * kTile) : t * kTile; }
   __device__ int end(int t) const { return head > 0 && t == 0 ? head : min(V, start(t) + kTile); }
-  // lane's 4 vectors of tile t: vector j covers elements start + (j*32 + lane)*VEC ..; elements past
+  // lane's vectors of tile t: vector j covers elements start + (j*32 + lane)*VEC ..; elements past
   // the tile's end read as -inf
-  __device__ __forceinline__ void load(int t, int lane, uint4 (&v)[4]) const {
+  __device__ __forceinline__ void load(int t, int lane, uint4 (&v)[kLoads]) const {
     const int s = start(t), len = end(t) - s;
     if (len == kTile) {
       const uint4* q = reinterpret_cast<const uint4*>(p + s) + lane;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] = __ldg(q + j * 32);
+      for (int j = 0; j < kLoads; ++j) v[j] = __ldg(q + j * 32);
     } else {
       load_edge(s, len, lane, v);
     }
   }
-  __device__ __forceinline__ void load_edge(int s, int len, int lane, uint4 (&v)[4]) const {
+  // the tile after the last full one
+  __device__ int full_end() const { return (head > 0 ? 1 : 0) + (V - head) / kTile; }
+  __device__ __forceinline__ void load_edge(int s, int len, int lane, uint4 (&v)[kLoads]) const {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < kLoads; ++j) {
       T e[E::kVec];
 #pragma unroll
       for (int i = 0; i < E::kVec; ++i) {
@@ -177,31 +178,157 @@ struct RowTiles {
   }
 };
 
-struct CtaPart {  // a CTA's sums: maximum, sum 2^x and sum 2^x x against it
-  double S, E;
-  float R;
+struct CtaPart {  // a CTA's sums against its maximum: sum 2^x and sum 2^x x
+  float S, E, R;
   int bad;
 };
 
+// Packed fp32 pairs (sm_100): the same correctly rounded results as the scalar instructions, at half
+// the instruction count.
+__device__ __forceinline__ float2 p_add(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 ra, rb, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+      "add.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 p_mul(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 ra, rb, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+      "mul.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 p_fma(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 ra, rb, rc, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+      "mov.b64 rc, {%6, %7};\n\tfma.rn.f32x2 rd, ra, rb, rc;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float redux_max(float v) {
+  float d;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(d) : "f"(v));
+  return d;
+}
+
+// Nothing below 2^kFloor of the maximum is added; the clamp also keeps 0 * inf out of E.
+constexpr float kFloor = -200.f;
+
+// Sums against different maxima joined over the lanes of a warp.
+__device__ __forceinline__ CtaPart join_parts(CtaPart p, float c) {
+  const float M = redux_max(p.R);
+  float S = 0.f, E = 0.f;
+  if (p.R > -INFINITY) {
+    const float dr = fmaxf((p.R - M) * c, kFloor), f = exp2f(dr);
+    S = p.S * f;
+    E = fmaf(p.S, dr, p.E) * f;
+  }
+  return CtaPart{warp_sum_f(S), warp_sum_f(E), M, __any_sync(0xffffffffu, p.bad)};
+}
+
+// A warp's running sums over the tiles it takes.
 template <int DT>
-__global__ void __launch_bounds__(kLpThreads, 2) token_logprobs_kernel(LpArgs a) {
+struct WarpSums {
+  using E = Elem<DT>;
+  static constexpr int kPairs = E::kVec / 2, kLoads = RowTiles<DT>::kLoads;
+  static constexpr int kAhead = 1;
+  float c, R;
+  float2 S2, E2;
+  int bad;
+  __device__ explicit WarpSums(float c_)
+      : c(c_), R(-INFINITY), S2(make_float2(0.f, 0.f)), E2(make_float2(0.f, 0.f)), bad(0) {}
+
+  // One tile into the sums; false if they are no longer numbers.  Masked values (0 * -inf in E) and NaN
+  // need CLAMP; rows without them, most, go without its two instructions a pair.
+  template <bool CLAMP>
+  __device__ __forceinline__ bool tile(const uint4 (&v)[kLoads], int lane, float* max_out) {
+    float m = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j)
+#pragma unroll
+      for (int i = 0; i < kPairs; ++i) {
+        const float2 x = E::pair(v[j], i);
+        m = max3_nan(m, x.x, x.y);
+      }
+    m = warp_max_nan(m);
+    if (lane == 0) *max_out = m;
+    if (CLAMP) bad |= !(m < INFINITY);  // NaN or +inf
+    if (m > R) {                        // the same for all lanes
+      const float dr = fmaxf((R - m) * c, kFloor), f = ex2(dr);  // R = -inf: S = E = 0 stay
+      E2 = p_mul(p_fma(S2, make_float2(dr, dr), E2), make_float2(f, f));
+      S2 = p_mul(S2, make_float2(f, f));
+      R = m;
+    }
+    if (CLAMP && R == -INFINITY) return true;
+    const float2 nR = make_float2(-R, -R), c2 = make_float2(c, c);
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j)
+#pragma unroll
+      for (int i = 0; i < kPairs; ++i) {
+        float2 d = p_mul(p_add(E::pair(v[j], i), nR), c2);
+        if (CLAMP) d = make_float2(fmaxf(d.x, kFloor), fmaxf(d.y, kFloor));
+        const float2 e = make_float2(ex2(d.x), ex2(d.y));
+        S2 = p_add(S2, e);
+        E2 = p_fma(e, d, E2);
+      }
+    if (CLAMP) return true;
+    const float x = E2.x + E2.y;
+    return !__any_sync(0xffffffffu, x != x);
+  }
+
+  // Full tiles t, t + W, ... below end, the next kAhead tiles' loads in flight; false as tile().
+  template <bool CLAMP, int W>
+  __device__ __forceinline__ bool pass(const RowTiles<DT>& tiles, int t, int end, int lane, float* max_out) {
+    const uint4* src = reinterpret_cast<const uint4*>(tiles.p + tiles.start(t)) + lane;
+    uint4 buf[kAhead + 1][kLoads];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) fetch<W>(src, i, t, end, buf[i]);
+    while (t < end) {
+#pragma unroll
+      for (int u = 0; u <= kAhead; ++u)
+        if (t + u * W < end) {
+          fetch<W>(src, u + kAhead, t, end, buf[(u + kAhead) % (kAhead + 1)]);
+          if (!tile<CLAMP>(buf[u], lane, max_out + t + u * W)) return false;
+        }
+      t += (kAhead + 1) * W;
+      src += (kAhead + 1) * (W * 32 * kLoads);
+    }
+    return true;
+  }
+  template <int W>
+  static __device__ __forceinline__ void fetch(const uint4* src, int i, int t, int end, uint4 (&v)[kLoads]) {
+    if (t + i * W < end) {
+#pragma unroll
+      for (int j = 0; j < kLoads; ++j) v[j] = __ldcs(src + i * (W * 32 * kLoads) + j * 32);
+    }
+  }
+};
+
+template <int DT, int W>
+__global__ void __launch_bounds__(W * 32, 32 / W) token_logprobs_kernel(LpArgs a) {
   using E = Elem<DT>;
   using T = typename E::T;
-  constexpr int kPairs = E::kVec / 2;
-  __shared__ float s_max[kLpMaxTiles];
-  __shared__ uint64_t s_cand[kLpCand];
+  constexpr int kLoads = RowTiles<DT>::kLoads;
+  constexpr int kLpWarps = W, kLpThreads = W * 32;
+  // [top^2] candidates found by this CTA, the same again for the whole cluster's (C > 1), and the
+  // maxima of the row's tiles (all CTAs')
+  extern __shared__ __align__(16) uint8_t s_dyn[];
+  const int ncand = a.top * a.top;
+  uint64_t* s_cand = reinterpret_cast<uint64_t*>(s_dyn);
   __shared__ uint64_t s_top[DSPARK_TOP_MAX];
-  __shared__ uint64_t s_all[kLpMaxCluster * DSPARK_TOP_MAX];
-  __shared__ float s_R[kLpWarps], s_S[kLpWarps], s_E[kLpWarps];
-  __shared__ int s_bad[kLpWarps];
+  __shared__ CtaPart s_warp[kLpWarps];
   __shared__ int s_sel[DSPARK_TOP_MAX];
   __shared__ CtaPart s_part;
   __shared__ float s_thr;
-  __shared__ int s_nsel, s_ncand, s_ntop, s_nall;
+  __shared__ int s_nsel, s_ncand, s_nall;
   __shared__ double s_m, s_logS;
 
   cg::cluster_group cluster = cg::this_cluster();
-  const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  const int C = (int)cluster.num_blocks();
+  uint64_t* s_all = s_cand + ncand;
+  float* s_max = reinterpret_cast<float*>(s_cand + (C > 1 ? 2 : 1) * ncand);
+  const int rank = (int)cluster.block_rank();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const long long n = blockIdx.x / C;
   const int tok = __ldg(a.tokens + n);
@@ -226,166 +353,126 @@ __global__ void __launch_bounds__(kLpThreads, 2) token_logprobs_kernel(LpArgs a)
   }
 
   const RowTiles<DT> tiles(static_cast<const T*>(a.logits) + row * a.ld, a.V);
-  const int t0 = (int)((long long)tiles.n * rank / C), t1 = (int)((long long)tiles.n * (rank + 1) / C);
+  const int nt = tiles.n;
+  const int t0 = (int)((long long)nt * rank / C), t1 = (int)((long long)nt * (rank + 1) / C);
 
   // ---------------------------------------------------------------- one pass over the CTA's tiles
-  float R = -INFINITY;
-  float2 S2 = make_float2(0.f, 0.f), E2 = make_float2(0.f, 0.f);
-  int bad = 0;
-  uint4 cur[4], nxt[4];
-  if (t0 + warp < t1) tiles.load(t0 + warp, lane, cur);
-  for (int t = t0 + warp; t < t1; t += kLpWarps) {
-    if (t + kLpWarps < t1) tiles.load(t + kLpWarps, lane, nxt);
-    float m = -INFINITY;
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int i = 0; i < kPairs; ++i) {
-        const float2 x = E::pair(cur[j], i);
-        m = max3_nan(m, x.x, x.y);
-      }
-    m = warp_max_nan(m);
-    if (lane == 0) s_max[t - t0] = m;
-    if (!(m < INFINITY)) bad = 1;  // NaN or +inf
-    if (m > R) {  // the same for all lanes
-      if (R > -INFINITY) {
-        const float dr = (R - m) * a.c, f = ex2(fmaxf(dr, -200.f));
-        E2.x = (E2.x + S2.x * fmaxf(dr, -200.f)) * f;
-        E2.y = (E2.y + S2.y * fmaxf(dr, -200.f)) * f;
-        S2.x *= f;
-        S2.y *= f;
-      }
-      R = m;
+  // full tiles [b0, b1) of the CTA first, then what the row begins or ends with
+  const int b0 = max(t0, tiles.head > 0 ? 1 : 0), b1 = min(t1, tiles.full_end());
+  WarpSums<DT> sums(a.c);
+  if (!sums.template pass<false, W>(tiles, b0 + warp, b1, lane, s_max)) {
+    sums = WarpSums<DT>(a.c);
+    sums.template pass<true, W>(tiles, b0 + warp, b1, lane, s_max);
+  }
+  if (warp == W - 1) {
+    for (int e = 0; e < 2; ++e) {
+      const int t = e == 0 ? 0 : nt - 1;
+      if (t < t0 || t >= t1 || (t >= b0 && t < b1) || (e == 1 && nt == 1)) continue;
+      uint4 v[kLoads];
+      tiles.load_edge(tiles.start(t), tiles.end(t) - tiles.start(t), lane, v);
+      sums.template tile<true>(v, lane, s_max + t);
     }
-    if (m > -INFINITY) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int i = 0; i < kPairs; ++i) {
-          const float2 x = E::pair(cur[j], i);
-          // below 2^-200 nothing is added; the clamp also keeps 0 * inf out of E
-          const float dx = fmaxf((x.x - R) * a.c, -200.f), dy = fmaxf((x.y - R) * a.c, -200.f);
-          const float ex = ex2(dx), ey = ex2(dy);
-          S2.x += ex;
-          S2.y += ey;
-          E2.x = fmaf(ex, dx, E2.x);
-          E2.y = fmaf(ey, dy, E2.y);
-        }
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) cur[j] = nxt[j];
   }
   {
-    const float S = warp_sum_f(S2.x + S2.y), Es = warp_sum_f(E2.x + E2.y);
-    if (lane == 0) {
-      s_R[warp] = R;
-      s_S[warp] = S;
-      s_E[warp] = Es;
-      s_bad[warp] = bad;
-    }
+    const float S = warp_sum_f(sums.S2.x + sums.S2.y), Es = warp_sum_f(sums.E2.x + sums.E2.y);
+    if (lane == 0) s_warp[warp] = CtaPart{S, Es, sums.R, sums.bad};
   }
-  if (tid == 0) s_ncand = 0;
+  if (tid == 0) s_ncand = s_nall = 0;
   __syncthreads();
-
-  // ---------------------------------------------------------------- the CTA's sums; its best tiles
-  const double cd = a.inv_T * kLog2eD;
   if (warp == 1) {
-    const float r = lane < kLpWarps ? s_R[lane] : -INFINITY;
-    const float M = warp_max(r);
-    const int b = __any_sync(0xffffffffu, lane < kLpWarps && s_bad[lane]);
-    double S = 0.0, Es = 0.0;
-    if (lane < kLpWarps && r > -INFINITY) {
-      const double dr = fmax(((double)r - (double)M) * cd, -1000.0), f = exp2(dr);
-      S = (double)s_S[lane] * f;
-      Es = ((double)s_E[lane] + (double)s_S[lane] * dr) * f;
-    }
-    S = warp_sum_d(S);
-    Es = warp_sum_d(Es);
-    if (lane == 0) s_part = CtaPart{S, Es, M, b};
+    const CtaPart p = join_parts(lane < kLpWarps ? s_warp[lane] : CtaPart{0.f, 0.f, -INFINITY, 0}, a.c);
+    if (lane == 0) s_part = p;
   }
-  if (warp == 0 && a.top > 0) {
-    const int nt = t1 - t0;
-    int nsel = 0;
-    float last = -INFINITY, best = -INFINITY;
-    int bi = 0x7FFFFFFF;
-    auto scan = [&] {
-      best = -INFINITY;
-      bi = 0x7FFFFFFF;
-      for (int i = lane; i < nt; i += 32)
-        if (s_max[i] > best) {
-          best = s_max[i];
-          bi = i;
-        }
-    };
-    scan();
-    while (nsel < a.top) {
-      const float M = warp_max(best);
-      if (!(M > -INFINITY)) break;
-      const int w = (int)__reduce_min_sync(0xffffffffu, best == M ? (unsigned)bi : 0x7FFFFFFFu);
-      if (lane == 0) s_sel[nsel] = w;
-      ++nsel;
-      last = M;
-      if ((w & 31) == lane) {
-        s_max[w] = -INFINITY;
-        scan();
-      }
-      __syncwarp();
-    }
-    if (lane == 0) {
-      s_nsel = nsel;
-      s_thr = nsel == a.top ? last : -INFINITY;  // every element to come is at or above it
-    }
-  }
-  __syncthreads();
 
   if (a.top > 0) {
-    // -------------------------------------------------------------- candidates of the best tiles
-    const int nsel = s_nsel;
-    const float thr = s_thr;
-    for (int j = warp; j < nsel; j += kLpWarps) {
-      const int t = t0 + s_sel[j];
-      const int ts = tiles.start(t);
-      uint4 v[4];
-      tiles.load(t, lane, v);
-      float x[4 * E::kVec];
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-#pragma unroll
-        for (int i = 0; i < kPairs; ++i) {
-          const float2 f = E::pair(v[q], i);
-          x[q * E::kVec + 2 * i] = f.x;
-          x[q * E::kVec + 2 * i + 1] = f.y;
+    // -------------------------------------------------------------- the row's best tiles
+    if (C > 1) {  // every CTA takes the others' maxima and makes the same choice
+      cluster.sync();
+      for (int t = tid; t < nt; t += kLpThreads)
+        if (t < t0 || t >= t1) {
+          // the CTA whose range holds t
+          int r = (int)(((long long)t * C) / nt);
+          while ((int)((long long)nt * (r + 1) / C) <= t) ++r;
+          s_max[t] = *cluster.map_shared_rank(s_max + t, r);
         }
-      for (int round = 0; round < a.top; ++round) {
-        float best = -INFINITY;
-        int bi = 0x7FFFFFFF;
-#pragma unroll
-        for (int q = 0; q < 4 * E::kVec; ++q)
-          if (x[q] > best) {  // in index order: the first of equal values stays
-            best = x[q];
-            bi = ((q / E::kVec) * 32 + lane) * E::kVec + q % E::kVec;
+      cluster.sync();  // (also a block barrier) nobody changes its maxima before all have them
+    }
+    if (warp == 0) {
+      int nsel = 0;
+      float last = -INFINITY, best;
+      int bi;
+      auto scan = [&] {
+        best = -INFINITY;
+        bi = 0x7FFFFFFF;
+        for (int i = lane; i < nt; i += 32)
+          if (s_max[i] > best) {
+            best = s_max[i];
+            bi = i;
           }
-        const float M = warp_max(best);
-        if (!(M > -INFINITY) || M < thr) break;
+      };
+      scan();
+      while (nsel < a.top) {
+        const float M = redux_max(best);
+        if (!(M > -INFINITY)) break;
         const int w = (int)__reduce_min_sync(0xffffffffu, best == M ? (unsigned)bi : 0x7FFFFFFFu);
-        if (lane == 0) s_cand[atomicAdd(&s_ncand, 1)] = cand_key(M, (uint32_t)(ts + w));
-        if (best == M && bi == w) {
-#pragma unroll
-          for (int q = 0; q < 4 * E::kVec; ++q)
-            if (((q / E::kVec) * 32 + lane) * E::kVec + q % E::kVec == w) x[q] = -INFINITY;
+        if (lane == 0) s_sel[nsel] = w;
+        ++nsel;
+        last = M;
+        if ((w & 31) == lane) {
+          s_max[w] = -INFINITY;
+          scan();
         }
+        __syncwarp();
+      }
+      if (lane == 0) {
+        s_nsel = nsel;
+        s_thr = nsel == a.top ? last : -INFINITY;  // every element to come is at or above it
       }
     }
     __syncthreads();
-    // rank by counting (the keys are distinct): key i goes to place #{j : key j > key i}
-    const int nc = s_ncand;
-    for (int i = tid; i < nc; i += kLpThreads) {
-      const uint64_t k = s_cand[i];
-      int place = 0;
-      for (int j = 0; j < nc; ++j) place += s_cand[j] > k;
-      if (place < a.top) s_top[place] = k;
+
+    // -------------------------------------------------------------- their candidates
+    const int nsel = s_nsel;
+    const float thr = s_thr;
+    for (int j = warp * C + rank; j < nsel; j += kLpWarps * C) {
+      const int t = s_sel[j], ts = tiles.start(t);
+      uint4 v[kLoads];
+      tiles.load(t, lane, v);
+      auto value = [&](int q) {
+        const float2 f = E::pair(v[q / E::kVec], (q % E::kVec) / 2);
+        return (q & 1) ? f.y : f.x;
+      };
+      auto index = [&](int q) { return ((q / E::kVec) * 32 + lane) * E::kVec + q % E::kVec; };
+      uint32_t in = 0;  // this lane's values at or above the threshold
+#pragma unroll
+      for (int q = 0; q < kLoads * E::kVec; ++q)
+        if (value(q) >= thr && value(q) > -INFINITY) in |= 1u << q;
+      const int all = __reduce_add_sync(0xffffffffu, __popc(in));
+      if (all <= a.top) {
+        if (in) {
+          int at = atomicAdd(&s_ncand, __popc(in));
+#pragma unroll
+          for (int q = 0; q < kLoads * E::kVec; ++q)
+            if (in >> q & 1) s_cand[at++] = cand_key(value(q), (uint32_t)(ts + index(q)));
+        }
+      } else {  // more than `top`: take the best ones in turn
+        for (int round = 0; round < a.top; ++round) {
+          float best = -INFINITY;
+          int bq = -1;
+#pragma unroll
+          for (int q = 0; q < kLoads * E::kVec; ++q)
+            if ((in >> q & 1) && value(q) > best) {  // in index order: the first of equal values stays
+              best = value(q);
+              bq = q;
+            }
+          const float M = redux_max(best);
+          const int bi = bq < 0 ? 0x7FFFFFFF : index(bq);
+          const int w = (int)__reduce_min_sync(0xffffffffu, best == M ? (unsigned)bi : 0x7FFFFFFFu);
+          if (lane == 0) s_cand[atomicAdd(&s_ncand, 1)] = cand_key(M, (uint32_t)(ts + w));
+          if (bi == w) in &= ~(1u << bq);
+        }
+      }
     }
-    if (tid == 0) s_ntop = min(nc, a.top);
   }
 
   // ---------------------------------------------------------------- join the cluster, write the row
@@ -393,41 +480,33 @@ __global__ void __launch_bounds__(kLpThreads, 2) token_logprobs_kernel(LpArgs a)
   else __syncthreads();
   if (rank == 0) {
     if (warp == 0) {
-      CtaPart p{0.0, 0.0, -INFINITY, 0};
+      CtaPart p{0.f, 0.f, -INFINITY, 0};
       if (lane < C) p = C > 1 ? *cluster.map_shared_rank(&s_part, lane) : s_part;
-      const float M = warp_max(p.R);
-      const int b = __any_sync(0xffffffffu, p.bad);
-      double S = 0.0, Es = 0.0;
-      if (p.R > -INFINITY) {
-        const double dr = fmax(((double)p.R - (double)M) * cd, -1000.0), f = exp2(dr);
-        S = p.S * f;
-        Es = (p.E + p.S * dr) * f;
-      }
-      S = warp_sum_d(S);
-      Es = warp_sum_d(Es);
+      if (C > 1) p = join_parts(p, a.c);
       if (lane == 0) {
+        p = C > 1 ? p : s_part;
         const float nan = __int_as_float(0x7FC00000);
-        double logS = log(S);
-        float lp, H, m = M;
+        double logS = log((double)p.S);
+        float lp, H, m = p.R;
         uint32_t fl = 0;
-        if (b) {
+        if (p.bad) {
           fl |= DSPARK_FLAG_NONFINITE;
           m = nan;
           logS = (double)nan;
           lp = H = nan;
-        } else if (!(M > -INFINITY)) {  // nothing in the row is unmasked
+        } else if (!(p.R > -INFINITY)) {  // nothing in the row is unmasked
           logS = -INFINITY;
           lp = -INFINITY;
           H = 0.f;
         } else {
-          H = (float)(logS - Es / S * kLn2D);
+          H = (float)(logS - (double)p.E / (double)p.S * kLn2D);
           lp = 0.f;
         }
         if ((unsigned)tok >= (unsigned)a.V) {
           fl |= DSPARK_FLAG_TOKEN_RANGE;
           lp = nan;
-        } else if (!b && M > -INFINITY) {
-          lp = (float)(((double)E::get(tiles.p[tok]) - (double)M) * a.inv_T - logS);
+        } else if (!p.bad && p.R > -INFINITY) {
+          lp = (float)(((double)E::get(tiles.p[tok]) - (double)p.R) * a.inv_T - logS);
         }
         a.logp[n] = lp;
         if (a.entropy) a.entropy[n] = H;
@@ -438,35 +517,33 @@ __global__ void __launch_bounds__(kLpThreads, 2) token_logprobs_kernel(LpArgs a)
       }
     }
     if (a.top > 0) {
-      const uint64_t* from = s_top;
-      int nc = s_ntop;
-      if (C > 1) {  // the CTAs' lists, ranked again
-        if (tid == 0) s_nall = 0;
-        __syncthreads();
+      const uint64_t* from = s_cand;
+      int nc = s_ncand;
+      if (C > 1) {
         for (int r = warp; r < C; r += kLpWarps) {
-          const int k = *cluster.map_shared_rank(&s_ntop, r);
-          const uint64_t* src = cluster.map_shared_rank(s_top, r);
+          const int k = *cluster.map_shared_rank(&s_ncand, r);
+          const uint64_t* src = cluster.map_shared_rank(s_cand, r);
           int at = 0;
-          if (lane == 0) at = atomicAdd(&s_nall, k);
+          if (lane == 0 && k) at = atomicAdd(&s_nall, k);
           at = __shfl_sync(0xffffffffu, at, 0);
-          if (lane < k) s_all[at + lane] = src[lane];
+          for (int i = lane; i < k; i += 32) s_all[at + i] = src[i];
         }
         __syncthreads();
-        const int na = s_nall;
-        for (int i = tid; i < na; i += kLpThreads) {
-          const uint64_t k = s_all[i];
-          int place = 0;
-          for (int j = 0; j < na; ++j) place += s_all[j] > k;
-          if (place < a.top) s_cand[place] = k;
-        }
-        from = s_cand;
-        nc = min(na, a.top);
+        from = s_all;
+        nc = s_nall;
+      }
+      // rank by counting (the keys are distinct): key i goes to place #{j : key j > key i}
+      for (int i = tid; i < nc; i += kLpThreads) {
+        const uint64_t k = from[i];
+        int place = 0;
+        for (int j = 0; j < nc; ++j) place += from[j] > k;
+        if (place < a.top) s_top[place] = k;
       }
       __syncthreads();
       const bool nan_row = isnan(s_m);
       if (tid < a.top) {
         const bool have = tid < nc && !nan_row;
-        const uint64_t k = have ? from[tid] : 0;
+        const uint64_t k = have ? s_top[tid] : 0;
         a.top_idx[n * a.top + tid] = have ? (int32_t)~(uint32_t)k : -1;
         a.top_logp[n * a.top + tid] = have      ? (float)(((double)key_value(k) - s_m) * a.inv_T - s_logS)
                                       : nan_row ? __int_as_float(0x7FC00000)
@@ -617,39 +694,43 @@ __global__ void __launch_bounds__(kLbThreads) token_logprobs_bwd_kernel(LbArgs a
 
 // ============================================================================ host
 
+template <int DT, int W>
+static cudaError_t launch_lp(const LpArgs& a, int N, int C, int nt, cudaStream_t st) {
+  auto kern = token_logprobs_kernel<DT, W>;
+  const size_t smem = (size_t)(C > 1 ? 2 : 1) * a.top * a.top * 8 + (size_t)nt * 4;
+  cudaError_t rc = ensure_smem_attr((const void*)kern, smem);
+  if (rc == cudaSuccess && C > 8) rc = ensure_nonportable_cluster((const void*)kern);
+  if (rc != cudaSuccess) return rc;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((long long)N * C));
+  cfg.blockDim = dim3(W * 32);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = C;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, a);
+}
+
 template <int DT>
 static dspark_status launch_lp(const LogprobsCall& c) {
   constexpr int kTile = RowTiles<DT>::kTile;
   const long long nt = ((long long)c.V + kTile - 1) / kTile + 1;
   // CTAs per row: while the rows alone leave SMs idle (two CTAs of 16 warps per SM), split each row,
-  // down to one tile a warp; more where a CTA could not hold the tiles' records
+  // down to one tile a warp
   const long long slots = 2ll * device_sm_count();
   int C = 1;
-  while (C < kLpMaxCluster && ((long long)c.N * 2 * C <= slots && nt / (2 * C) >= kLpWarps)) C *= 2;
-  while (C < kLpMaxCluster && (nt + C - 1) / C > kLpMaxTiles) C *= 2;
-  LpArgs a{c.logits, c.ld, c.rows, c.n_rows, c.tokens, c.V, c.top, 1.0 / (double)c.T, (float)(kLog2eD / (double)c.T),
+  while (C < kLpMaxCluster && (long long)c.N * 2 * C <= slots && nt / (2 * C) >= 16) C *= 2;
+  LpArgs a{c.logits, c.ld, c.rows, c.n_rows, c.tokens, c.V, c.top, 1.0 / (double)c.T, (float)(1.0 / (kLn2D * (double)c.T)),
            c.logp, c.entropy, c.top_idx, c.top_logp, reinterpret_cast<float2*>(c.stats), c.flags};
-  auto kern = token_logprobs_kernel<DT>;
-  cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(kLpThreads);
-  cfg.stream = c.stream;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  cudaError_t rc = cudaSuccess;
-  if (C > 8 && ensure_nonportable_cluster((const void*)kern) != cudaSuccess) {
+  cudaError_t rc = C > 1 ? launch_lp<DT, 16>(a, c.N, C, (int)nt, c.stream) : launch_lp<DT, 8>(a, c.N, C, (int)nt, c.stream);
+  if (rc != cudaSuccess && C > 8) {  // no clusters of 16 here
     cudaGetLastError();
-    C = 8;
+    rc = launch_lp<DT, 16>(a, c.N, 8, (int)nt, c.stream);
   }
-  if ((nt + C - 1) / C > kLpMaxTiles) {
-    set_error("dspark_token_logprobs: V too large for the clusters this device allows");
-    return DSPARK_ENOTIMPL;
-  }
-  at[0].val.clusterDim.x = C;
-  cfg.gridDim = dim3((unsigned)((long long)c.N * C));
-  rc = cudaLaunchKernelEx(&cfg, kern, a);
   if (rc != cudaSuccess) {
     cudaGetLastError();
     set_error(std::string("token_logprobs launch: ") + cudaGetErrorString(rc));

@@ -19,6 +19,7 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <mutex>
 #include <string>
 
 #include "common.cuh"
@@ -239,6 +240,25 @@ static cudaError_t launch_mq(const CUtensorMap& mW, const CUtensorMap& mX, const
   return cudaGetLastError();
 }
 
+// A 2-D tensor map of a [rows, K] byte matrix in boxes of box_rows x 128 bytes, 128-byte swizzle.
+static bool byte_map(CUtensorMap* m, const int8_t* base, uint64_t K, uint64_t rows, uint64_t ld, uint32_t box_rows) {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    cudaDriverEntryPointQueryResult q;
+    void* p = nullptr;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  });
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {K, rows}, strides[1] = {ld};
+  const cuuint32_t box[2] = {(cuuint32_t)kMqKB, box_rows}, es[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<int8_t*>(base), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace
 
 dspark_status launch_matmul_q8(const MatmulQ8Call& c) {
@@ -273,11 +293,7 @@ dspark_status launch_matmul_q8(const MatmulQ8Call& c) {
   a.bars = a.stages * a.stage_bytes + slack;
   const size_t smem = 1024 + a.bars + misc;
   CUtensorMap mW, mX;
-  const uint64_t wd[2] = {(uint64_t)c.K, (uint64_t)c.N}, xd[2] = {(uint64_t)c.K, (uint64_t)c.M};
-  const uint64_t ws[1] = {(uint64_t)c.ldw}, xs[1] = {(uint64_t)c.ldq};
-  const uint32_t wb[2] = {(uint32_t)kMqKB, (uint32_t)a.bv}, xb[2] = {(uint32_t)kMqKB, (uint32_t)a.bn};
-  if (!encode_tensor_map_u8(&mW, const_cast<int8_t*>(c.w), wd, ws, wb) ||
-      !encode_tensor_map_u8(&mX, const_cast<int8_t*>(c.q), xd, xs, xb)) {
+  if (!byte_map(&mW, c.w, c.K, c.N, c.ldw, a.bv) || !byte_map(&mX, c.q, c.K, c.M, c.ldq, a.bn)) {
     set_error("dspark_matmul_q8: cuTensorMapEncodeTiled failed");
     return DSPARK_ECUDA;
   }
