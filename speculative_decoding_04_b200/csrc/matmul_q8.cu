@@ -34,6 +34,7 @@ constexpr int kMqEpiWarps = 8;
 constexpr int kMqKB = 128;  // bytes (= values) of K per stage
 constexpr int kMqMaxStages = 8;
 constexpr uint32_t kMqSmem = 227u * 1024u;
+constexpr int kPairMinTokens = 128;  // more tokens than this: CTA pairs
 
 struct MqArgs {
   const float* q_scale;
@@ -230,6 +231,238 @@ __global__ void __launch_bounds__(kMqThreads, 1)
   if (warp == 2) tmem_dealloc(tmem, a.tmem_cols);
 }
 
+// ---------------------------------------------------------------------------- CTA pairs
+//
+// The same product for many tokens: a cluster of two CTAs shares one tile of 256 weight rows by bn
+// tokens (tcgen05.mma.cta_group::2, M = 256).  Each CTA loads its 128 weight rows and half of the
+// tokens, so a tile's operands cross from L2 to shared memory once per pair, and holds the accumulators
+// of its rows: bn columns of tensor memory, twice, so that the epilogue of one tile runs beside the
+// products of the next.  Rank 0 issues the MMAs; both CTAs' loads complete on rank 0's full barriers,
+// and the commits arrive on both CTAs' empty and accumulator barriers.
+
+constexpr int kPairThreads = 384;
+constexpr int kPairEpiWarps = 8;
+constexpr int kPairMaxStages = 8;
+
+__device__ __forceinline__ uint32_t mapa_rank(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync_all() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+// Load into this CTA's shared memory, completing on a barrier of either CTA of the pair.
+__device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
+      "[%4];" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void tc_mma_i8_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                               uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Arrive on the barrier at this offset in both CTAs once the MMAs issued so far are done.
+__device__ __forceinline__ void tc_commit_pair(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_u32(bar)),
+      "h"((uint16_t)3)
+      : "memory");
+}
+
+// 32 lanes x 32 consecutive 32-bit columns (no wait).
+__device__ __forceinline__ void tmem_ld_x32(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+
+template <int DT>
+__global__ void __launch_bounds__(kPairThreads, 1)
+    matmul_q8_pair(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, MqArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint64_t* full = reinterpret_cast<uint64_t*>(sm + a.bars);  // (rank 0) both CTAs' loads of a stage
+  uint64_t* empty = full + kPairMaxStages;                    // the stage's MMAs are done
+  uint64_t* t_full = empty + kPairMaxStages;                  // [2] an accumulator is complete
+  uint64_t* t_empty = t_full + 2;                             // [2] (rank 0) both CTAs have read it
+  uint64_t* drain = t_empty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const MqSync sy{s_abort};
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint32_t rank;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+  const int nkb = (a.K + kMqKB - 1) / kMqKB;
+  const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+  const int half = a.bn >> 1;  // tokens this CTA loads
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < a.stages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&t_full[i], 1);
+      mbar_init(&t_empty[i], 2 * kPairEpiWarps);
+    }
+    mbar_init(drain, 1);
+    *s_abort = 0;
+    fence_mbar_init();
+    prefetch_tmap(&tmW);
+    prefetch_tmap(&tmX);
+  }
+  if (warp == 2) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                 "r"((uint32_t)a.tmem_cols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();  // the peer's barriers are initialised before anything arrives on them
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int it = 0;
+      bool ok = true;
+      for (int t = pair; ok && t < a.ntiles; t += npairs) {
+        const int v0 = (t / a.ntok) * 256 + (int)rank * 128, m0 = (t % a.ntok) * a.bn + (int)rank * half;
+        for (int k = 0; k < nkb; ++k, ++it) {
+          const int s = it % a.stages;
+          if (!mq_wait(sy, &empty[s], ((it / a.stages) & 1) ^ 1)) {
+            ok = false;
+            break;
+          }
+          uint8_t* st = sm + s * a.stage_bytes;
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], (uint32_t)(256 + a.bn) * kMqKB);
+          const uint32_t bar = mapa_rank(smem_u32(&full[s]), 0);
+          tma_load_2d_pair(st, &tmW, k * kMqKB, v0, bar);
+          tma_load_2d_pair(st + a.w_bytes, &tmX, k * kMqKB, m0, bar);
+        }
+      }
+      // after a timeout, rank 0 lets the copies of both CTAs land (bounded); rank 1 waits for it at the
+      // last cluster barrier
+      if (*s_abort && rank == 0)
+        for (int i = max(0, it - a.stages); i < it; ++i)
+          for (uint32_t n = 0; n < kSpinLimit && !mbar_try_wait(&full[i % a.stages], (i / a.stages) & 1); ++n) {
+          }
+    }
+  } else if (warp == 1) {
+    if (rank == 0 && lane == 0) {
+      const uint32_t idesc = (2u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(a.bn >> 3) << 17) |
+                             ((uint32_t)(256 >> 4) << 24);
+      int it = 0, n = 0;
+      bool ok = true;
+      for (int t = pair; ok && t < a.ntiles; t += npairs, ++n) {
+        const int buf = n & 1;
+        if (!mq_wait(sy, &t_empty[buf], ((n >> 1) & 1) ^ 1)) break;
+        tc_fence_after();
+        const uint32_t acc = tmem + (uint32_t)(buf * a.bn);
+        for (int k = 0; k < nkb; ++k, ++it) {
+          const int s = it % a.stages;
+          if (!mq_wait(sy, &full[s], (it / a.stages) & 1)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t w = smem_u32(sm + s * a.stage_bytes), x = w + a.w_bytes;
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            tc_mma_i8_pair(acc, smem_desc(w + kk * 32u, 16u, 1024u, 2u), smem_desc(x + kk * 32u, 16u, 1024u, 2u), idesc,
+                           (k | kk) != 0 ? 1u : 0u);
+          tc_commit_pair(&empty[s]);
+        }
+        if (ok) tc_commit_pair(&t_full[buf]);
+      }
+      if (*s_abort) {  // tensor memory and the stages stay until the MMAs already issued are done (bounded)
+        tc_commit_pair(drain);
+        mbar_wait(drain, 0);
+      }
+    }
+  } else if (warp >= 4) {
+    const int q = warp & 3, h = (warp - 4) >> 2;  // lane quadrant; which chunks of 32 columns
+    int n = 0;
+    for (int t = pair; t < a.ntiles; t += npairs, ++n) {
+      const int buf = n & 1;
+      const int v = (t / a.ntok) * 256 + (int)rank * 128 + q * 32 + lane, m0 = (t % a.ntok) * a.bn;
+      const bool mine = v < a.N;
+      const float sw = mine ? __ldg(a.w_scale + v) : 0.f;
+      const int nm = min(a.bn, a.M - m0);
+      const bool ok = __all_sync(0xffffffffu, mq_wait(sy, &t_full[buf], (n >> 1) & 1));
+      tc_fence_after();
+      const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * a.bn);
+      for (int c = h * 32; c < nm; c += 64) {
+        uint32_t r[32];
+        const float sq = c + lane < nm ? __ldg(a.q_scale + m0 + c + lane) : 0.f;
+        if (ok) {
+          tmem_ld_x32(acc + c, r);
+          tmem_wait_ld();
+        }
+        long long o = (long long)(m0 + c) * a.ldo + v;
+#pragma unroll
+        for (int j = 0; j < 32; ++j, o += a.ldo) {
+          const float s = __shfl_sync(0xffffffffu, sq, j);
+          if (c + j < nm && mine)
+            store_out<DT>(a.out, o, ok ? (float)(int32_t)r[j] * s * sw : __int_as_float(0x7FC00000));
+        }
+      }
+      if (!ok && a.flags && q == 0 && h == 0)
+        for (int m = m0 + lane; m < m0 + nm; m += 32) atomicOr(a.flags + m, DSPARK_FLAG_DEVICE_TIMEOUT);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(mapa_rank(smem_u32(&t_empty[buf]), 0));
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();  // neither CTA leaves while the other may still reach its memory
+  if (warp == 2)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"((uint32_t)a.tmem_cols)
+                 : "memory");
+}
+
+template <int DT>
+static cudaError_t launch_pair(const CUtensorMap& mW, const CUtensorMap& mX, const MqArgs& a, int grid, size_t smem,
+                               cudaStream_t st) {
+  auto kern = matmul_q8_pair<DT>;
+  cudaError_t rc = ensure_smem_attr((const void*)kern, smem);
+  if (rc != cudaSuccess) return rc;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kPairThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = 2;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, mW, mX, a);
+}
+
 template <int DT>
 static cudaError_t launch_mq(const CUtensorMap& mW, const CUtensorMap& mX, const MqArgs& a, int grid, size_t smem,
                              cudaStream_t st) {
@@ -273,36 +506,61 @@ dspark_status launch_matmul_q8(const MatmulQ8Call& c) {
   a.M = c.M;
   a.N = c.N;
   a.K = c.K;
-  a.ntok = (c.M + 255) / 256;
-  a.bn = ((c.M + a.ntok - 1) / a.ntok + 15) / 16 * 16;
-  // weight rows per tile: the largest tile that gives every CTA the same number of tiles
-  const int per = std::max(1, (int)(((long long)c.N * a.ntok + 256ll * sms - 1) / (256ll * sms)));
-  long long rows = ((long long)c.N * a.ntok + (long long)sms * per - 1) / ((long long)sms * per);
-  a.bv = (int)std::min(256ll, std::max(16ll, (rows + 15) / 16 * 16));
-  a.ntiles = a.ntok * ((c.N + a.bv - 1) / a.bv);
-  a.blocks = a.bv > 128 ? 2 : 1;
-  a.nbuf = 2 * a.blocks * a.bn <= 512 ? 2 : 1;
-  a.tmem_cols = 32;
-  while (a.tmem_cols < a.nbuf * a.blocks * a.bn) a.tmem_cols *= 2;
-  a.w_bytes = (uint32_t)(a.bv * kMqKB + 1023) / 1024 * 1024;
-  a.stage_bytes = a.w_bytes + (uint32_t)(a.bn * kMqKB + 1023) / 1024 * 1024;
-  // an MMA reads 128 weight rows whatever the tile holds: what follows the last stage is readable
-  const uint32_t slack = (uint32_t)(a.blocks * 16384) > a.stage_bytes ? a.blocks * 16384 - a.stage_bytes : 0;
+  const bool pair = c.M > kPairMinTokens;
   const uint32_t misc = 8 * (2 * kMqMaxStages + 5) + 16;
-  a.stages = (int)std::min<uint32_t>(kMqMaxStages, (kMqSmem - 1024 - misc - slack) / a.stage_bytes);
-  a.bars = a.stages * a.stage_bytes + slack;
+  const int step = pair ? 32 : 16;
+  a.ntok = (c.M + 255) / 256;
+  a.bn = ((c.M + a.ntok - 1) / a.ntok + step - 1) / step * step;
+  int box_v, box_m, grid;
+  if (pair) {
+    a.bv = 256;
+    a.ntiles = a.ntok * ((c.N + 255) / 256);
+    a.tmem_cols = 32;
+    while (a.tmem_cols < 2 * a.bn) a.tmem_cols *= 2;
+    a.w_bytes = 128 * kMqKB;
+    a.stage_bytes = a.w_bytes + (uint32_t)(a.bn / 2 * kMqKB + 1023) / 1024 * 1024;
+    a.stages = (int)std::min<uint32_t>(kPairMaxStages, (kMqSmem - 1024 - misc) / a.stage_bytes);
+    a.bars = a.stages * a.stage_bytes;
+    box_v = 128;
+    box_m = a.bn / 2;
+    grid = 2 * std::min(sms / 2, a.ntiles);
+  } else {
+    // weight rows per tile: the largest tile that gives every CTA the same number of tiles
+    const int per = std::max(1, (int)(((long long)c.N * a.ntok + 256ll * sms - 1) / (256ll * sms)));
+    long long rows = ((long long)c.N * a.ntok + (long long)sms * per - 1) / ((long long)sms * per);
+    a.bv = (int)std::min(256ll, std::max(16ll, (rows + 15) / 16 * 16));
+    a.ntiles = a.ntok * ((c.N + a.bv - 1) / a.bv);
+    a.blocks = a.bv > 128 ? 2 : 1;
+    a.nbuf = 2 * a.blocks * a.bn <= 512 ? 2 : 1;
+    a.tmem_cols = 32;
+    while (a.tmem_cols < a.nbuf * a.blocks * a.bn) a.tmem_cols *= 2;
+    a.w_bytes = (uint32_t)(a.bv * kMqKB + 1023) / 1024 * 1024;
+    a.stage_bytes = a.w_bytes + (uint32_t)(a.bn * kMqKB + 1023) / 1024 * 1024;
+    // an MMA reads 128 weight rows whatever the tile holds: what follows the last stage is readable
+    const uint32_t slack = (uint32_t)(a.blocks * 16384) > a.stage_bytes ? a.blocks * 16384 - a.stage_bytes : 0;
+    a.stages = (int)std::min<uint32_t>(kMqMaxStages, (kMqSmem - 1024 - misc - slack) / a.stage_bytes);
+    a.bars = a.stages * a.stage_bytes + slack;
+    box_v = a.bv;
+    box_m = a.bn;
+    grid = std::min(sms, a.ntiles);
+  }
   const size_t smem = 1024 + a.bars + misc;
   CUtensorMap mW, mX;
-  if (!byte_map(&mW, c.w, c.K, c.N, c.ldw, a.bv) || !byte_map(&mX, c.q, c.K, c.M, c.ldq, a.bn)) {
+  if (!byte_map(&mW, c.w, c.K, c.N, c.ldw, box_v) || !byte_map(&mX, c.q, c.K, c.M, c.ldq, box_m)) {
     set_error("dspark_matmul_q8: cuTensorMapEncodeTiled failed");
     return DSPARK_ECUDA;
   }
-  const int grid = std::min(sms, a.ntiles);
   cudaError_t rc;
   switch (c.out_dtype) {
-    case DSPARK_F32: rc = launch_mq<DSPARK_F32>(mW, mX, a, grid, smem, c.stream); break;
-    case DSPARK_BF16: rc = launch_mq<DSPARK_BF16>(mW, mX, a, grid, smem, c.stream); break;
-    default: rc = launch_mq<DSPARK_F16>(mW, mX, a, grid, smem, c.stream); break;
+    case DSPARK_F32:
+      rc = pair ? launch_pair<DSPARK_F32>(mW, mX, a, grid, smem, c.stream) : launch_mq<DSPARK_F32>(mW, mX, a, grid, smem, c.stream);
+      break;
+    case DSPARK_BF16:
+      rc = pair ? launch_pair<DSPARK_BF16>(mW, mX, a, grid, smem, c.stream) : launch_mq<DSPARK_BF16>(mW, mX, a, grid, smem, c.stream);
+      break;
+    default:
+      rc = pair ? launch_pair<DSPARK_F16>(mW, mX, a, grid, smem, c.stream) : launch_mq<DSPARK_F16>(mW, mX, a, grid, smem, c.stream);
+      break;
   }
   if (rc != cudaSuccess) {
     set_error(std::string("matmul_q8 launch: ") + cudaGetErrorString(rc));
