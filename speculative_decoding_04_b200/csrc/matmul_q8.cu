@@ -31,7 +31,8 @@ namespace {
 
 constexpr int kMqThreads = 384;
 constexpr int kMqEpiWarps = 8;
-constexpr int kMqKB = 128;  // bytes (= values) of K per stage
+constexpr int kMqKB = 128;    // bytes (= values) of a block of K: one swizzled row
+constexpr int kMqBlocks = 2;  // blocks of K per stage
 constexpr int kMqMaxStages = 8;
 constexpr uint32_t kMqSmem = 227u * 1024u;
 constexpr int kPairMinTokens = 128;  // more tokens than this: CTA pairs
@@ -46,7 +47,16 @@ struct MqArgs {
   int bv, bn;          // tile: weight rows (multiple of 16, <= 256), tokens (multiple of 16, <= 256)
   int ntok, ntiles;    // token tiles; tiles in all
   int stages, nbuf, blocks, tmem_cols;
-  uint32_t w_bytes, stage_bytes, bars;  // offsets within the aligned shared memory
+  uint32_t w_bytes, x_bytes;            // one block of K: bytes of the tile's weights and tokens
+  uint32_t x_off, stage_bytes, bars;    // tokens within a stage; a stage; barriers after the stages
+};
+
+// Tensor maps of the weights and the tokens: [rows, K] with boxes of 128 bytes of K by the tile's rows,
+// and the same matrix as [K / 128][rows][128 bytes] with boxes of two blocks.  One copy of two blocks
+// streams faster than two of one (the copy engine's rate grows with the copy: pairs at 1088 x 151936 x
+// 4096, 684 -> PAIR3D us); the last odd or partial block comes by the first map, which ends at K.
+struct MqMaps {
+  CUtensorMap w, x, w3, x3;
 };
 
 struct MqSync {
@@ -95,7 +105,7 @@ __device__ __forceinline__ void store_out(void* out, long long i, float v) {
 
 template <int DT>
 __global__ void __launch_bounds__(kMqThreads, 1)
-    matmul_q8_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, MqArgs a) {
+    matmul_q8_kernel(const __grid_constant__ MqMaps tm, MqArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + a.bars);
@@ -121,8 +131,8 @@ __global__ void __launch_bounds__(kMqThreads, 1)
     mbar_init(drain, 1);
     *s_abort = 0;
     fence_mbar_init();
-    prefetch_tmap(&tmW);
-    prefetch_tmap(&tmX);
+    prefetch_tmap(&tm.w3);
+    prefetch_tmap(&tm.x3);
   }
   if (warp == 2) {
     tmem_alloc(tmem_slot, a.tmem_cols);
@@ -139,16 +149,24 @@ __global__ void __launch_bounds__(kMqThreads, 1)
       bool ok = true;
       for (int t = blockIdx.x; ok && t < a.ntiles; t += gridDim.x) {
         const int v0 = (t / a.ntok) * a.bv, m0 = (t % a.ntok) * a.bn;
-        for (int k = 0; k < nkb; ++k, ++it) {
+        for (int k = 0; k < nkb; k += kMqBlocks, ++it) {
           const int s = it % a.stages;
           if (!mq_wait(sy, &empty[s], ((it / a.stages) & 1) ^ 1)) {
             ok = false;
             break;
           }
           uint8_t* st = sm + s * a.stage_bytes;
-          mbar_arrive_expect_tx(&full[s], (uint32_t)(a.bv + a.bn) * kMqKB);
-          tma_load_2d(st, &tmW, k * kMqKB, v0, &full[s]);
-          tma_load_2d(st + a.w_bytes, &tmX, k * kMqKB, m0, &full[s]);
+          const int nb = min(kMqBlocks, nkb - k);
+          mbar_arrive_expect_tx(&full[s], (uint32_t)(a.bv + a.bn) * kMqKB * nb);
+          if ((k + kMqBlocks) * kMqKB <= a.K) {
+            tma_load_3d(st, &tm.w3, 0, v0, k, &full[s]);
+            tma_load_3d(st + a.x_off, &tm.x3, 0, m0, k, &full[s]);
+          } else {
+            for (int i = 0; i < nb; ++i) {
+              tma_load_2d(st + i * a.w_bytes, &tm.w, (k + i) * kMqKB, v0, &full[s]);
+              tma_load_2d(st + a.x_off + i * a.x_bytes, &tm.x, (k + i) * kMqKB, m0, &full[s]);
+            }
+          }
         }
       }
       if (*s_abort)  // let the copies already issued land (bounded) before the CTA exits
@@ -169,19 +187,23 @@ __global__ void __launch_bounds__(kMqThreads, 1)
         if (!mq_wait(sy, &t_empty[buf], ((n / a.nbuf) & 1) ^ 1)) break;
         tc_fence_after();
         const uint32_t acc = tmem + (uint32_t)(buf * a.blocks * a.bn);
-        for (int k = 0; k < nkb; ++k, ++it) {
+        for (int k = 0; k < nkb; k += kMqBlocks, ++it) {
           const int s = it % a.stages;
           if (!mq_wait(sy, &full[s], (it / a.stages) & 1)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t w = smem_u32(sm + s * a.stage_bytes), x = w + a.w_bytes;
-          for (int b = 0; b < a.blocks; ++b)
+          const uint32_t st = smem_u32(sm + s * a.stage_bytes);
+          const int nb = min(kMqBlocks, nkb - k);
+          for (int i = 0; i < nb; ++i) {
+            const uint32_t w = st + i * a.w_bytes, x = st + a.x_off + i * a.x_bytes;
+            for (int b = 0; b < a.blocks; ++b)
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              tc_mma_i8(acc + (uint32_t)(b * a.bn), smem_desc(w + b * 16384u + kk * 32u, 16u, 1024u, 2u),
-                        smem_desc(x + kk * 32u, 16u, 1024u, 2u), idesc, (k | kk) != 0 ? 1u : 0u);
+              for (int kk = 0; kk < 4; ++kk)
+                tc_mma_i8(acc + (uint32_t)(b * a.bn), smem_desc(w + b * 16384u + kk * 32u, 16u, 1024u, 2u),
+                          smem_desc(x + kk * 32u, 16u, 1024u, 2u), idesc, (k | i | kk) != 0 ? 1u : 0u);
+          }
           tc_commit(&empty[s]);
         }
         if (ok) tc_commit(&t_full[buf]);
@@ -263,6 +285,13 @@ __device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* m
       "l"(map), "r"(x), "r"(y), "r"(bar)
       : "memory");
 }
+__device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, "
+      "%4}], [%5];" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
 __device__ __forceinline__ void tc_mma_i8_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                                uint32_t accumulate) {
   asm volatile(
@@ -297,7 +326,7 @@ __device__ __forceinline__ void tmem_ld_x32(uint32_t taddr, uint32_t (&r)[32]) {
 
 template <int DT>
 __global__ void __launch_bounds__(kPairThreads, 1)
-    matmul_q8_pair(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, MqArgs a) {
+    matmul_q8_pair(const __grid_constant__ MqMaps tm, MqArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + a.bars);  // (rank 0) both CTAs' loads of a stage
@@ -327,8 +356,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     mbar_init(drain, 1);
     *s_abort = 0;
     fence_mbar_init();
-    prefetch_tmap(&tmW);
-    prefetch_tmap(&tmX);
+    prefetch_tmap(&tm.w3);
+    prefetch_tmap(&tm.x3);
   }
   if (warp == 2) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
@@ -348,17 +377,25 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       bool ok = true;
       for (int t = pair; ok && t < a.ntiles; t += npairs) {
         const int v0 = (t / a.ntok) * 256 + (int)rank * 128, m0 = (t % a.ntok) * a.bn + (int)rank * half;
-        for (int k = 0; k < nkb; ++k, ++it) {
+        for (int k = 0; k < nkb; k += kMqBlocks, ++it) {
           const int s = it % a.stages;
           if (!mq_wait(sy, &empty[s], ((it / a.stages) & 1) ^ 1)) {
             ok = false;
             break;
           }
           uint8_t* st = sm + s * a.stage_bytes;
-          if (rank == 0) mbar_arrive_expect_tx(&full[s], (uint32_t)(256 + a.bn) * kMqKB);
+          const int nb = min(kMqBlocks, nkb - k);
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], (uint32_t)(256 + a.bn) * kMqKB * nb);
           const uint32_t bar = mapa_rank(smem_u32(&full[s]), 0);
-          tma_load_2d_pair(st, &tmW, k * kMqKB, v0, bar);
-          tma_load_2d_pair(st + a.w_bytes, &tmX, k * kMqKB, m0, bar);
+          if ((k + kMqBlocks) * kMqKB <= a.K) {
+            tma_load_3d_pair(st, &tm.w3, 0, v0, k, bar);
+            tma_load_3d_pair(st + a.x_off, &tm.x3, 0, m0, k, bar);
+          } else {
+            for (int i = 0; i < nb; ++i) {
+              tma_load_2d_pair(st + i * a.w_bytes, &tm.w, (k + i) * kMqKB, v0, bar);
+              tma_load_2d_pair(st + a.x_off + i * a.x_bytes, &tm.x, (k + i) * kMqKB, m0, bar);
+            }
+          }
         }
       }
       // after a timeout, rank 0 lets the copies of both CTAs land (bounded); rank 1 waits for it at the
@@ -379,18 +416,22 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         if (!mq_wait(sy, &t_empty[buf], ((n >> 1) & 1) ^ 1)) break;
         tc_fence_after();
         const uint32_t acc = tmem + (uint32_t)(buf * a.bn);
-        for (int k = 0; k < nkb; ++k, ++it) {
+        for (int k = 0; k < nkb; k += kMqBlocks, ++it) {
           const int s = it % a.stages;
           if (!mq_wait(sy, &full[s], (it / a.stages) & 1)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t w = smem_u32(sm + s * a.stage_bytes), x = w + a.w_bytes;
+          const uint32_t st = smem_u32(sm + s * a.stage_bytes);
+          const int nb = min(kMqBlocks, nkb - k);
+          for (int i = 0; i < nb; ++i) {
+            const uint32_t w = st + i * a.w_bytes, x = st + a.x_off + i * a.x_bytes;
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            tc_mma_i8_pair(acc, smem_desc(w + kk * 32u, 16u, 1024u, 2u), smem_desc(x + kk * 32u, 16u, 1024u, 2u), idesc,
-                           (k | kk) != 0 ? 1u : 0u);
+            for (int kk = 0; kk < 4; ++kk)
+              tc_mma_i8_pair(acc, smem_desc(w + kk * 32u, 16u, 1024u, 2u), smem_desc(x + kk * 32u, 16u, 1024u, 2u), idesc,
+                             (k | i | kk) != 0 ? 1u : 0u);
+          }
           tc_commit_pair(&empty[s]);
         }
         if (ok) tc_commit_pair(&t_full[buf]);
@@ -444,7 +485,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 }
 
 template <int DT>
-static cudaError_t launch_pair(const CUtensorMap& mW, const CUtensorMap& mX, const MqArgs& a, int grid, size_t smem,
+static cudaError_t launch_pair(const MqMaps& tm, const MqArgs& a, int grid, size_t smem,
                                cudaStream_t st) {
   auto kern = matmul_q8_pair<DT>;
   cudaError_t rc = ensure_smem_attr((const void*)kern, smem);
@@ -460,21 +501,22 @@ static cudaError_t launch_pair(const CUtensorMap& mW, const CUtensorMap& mX, con
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, mW, mX, a);
+  return cudaLaunchKernelEx(&cfg, kern, tm, a);
 }
 
 template <int DT>
-static cudaError_t launch_mq(const CUtensorMap& mW, const CUtensorMap& mX, const MqArgs& a, int grid, size_t smem,
+static cudaError_t launch_mq(const MqMaps& tm, const MqArgs& a, int grid, size_t smem,
                              cudaStream_t st) {
   auto kern = matmul_q8_kernel<DT>;
   cudaError_t rc = ensure_smem_attr((const void*)kern, smem);
   if (rc != cudaSuccess) return rc;
-  kern<<<grid, kMqThreads, smem, st>>>(mW, mX, a);
+  kern<<<grid, kMqThreads, smem, st>>>(tm, a);
   return cudaGetLastError();
 }
 
-// A 2-D tensor map of a [rows, K] byte matrix in boxes of box_rows x 128 bytes, 128-byte swizzle.
-static bool byte_map(CUtensorMap* m, const int8_t* base, uint64_t K, uint64_t rows, uint64_t ld, uint32_t box_rows) {
+// The two tensor maps of a [rows, K] byte matrix (128-byte swizzle).
+static bool byte_maps(CUtensorMap* m, CUtensorMap* m3, const int8_t* base, uint64_t K, uint64_t rows, uint64_t ld,
+                      uint32_t box_rows) {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
   static std::once_flag once;
   std::call_once(once, [] {
@@ -485,11 +527,22 @@ static bool byte_map(CUtensorMap* m, const int8_t* base, uint64_t K, uint64_t ro
       fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
   });
   if (!fn) return false;
-  const cuuint64_t dims[2] = {K, rows}, strides[1] = {ld};
-  const cuuint32_t box[2] = {(cuuint32_t)kMqKB, box_rows}, es[2] = {1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<int8_t*>(base), dims, strides, box, es,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  auto enc = [&](CUtensorMap* to, int rank, const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box) {
+    const cuuint32_t es[3] = {1, 1, 1};
+    return fn(to, CU_TENSOR_MAP_DATA_TYPE_UINT8, rank, const_cast<int8_t*>(base), dims, strides, box, es,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  };
+  const cuuint64_t d2[2] = {K, rows}, s2[1] = {ld};
+  const cuuint32_t b2[2] = {(cuuint32_t)kMqKB, box_rows};
+  if (!enc(m, 2, d2, s2, b2)) return false;
+  if (K < kMqBlocks * kMqKB) {  // no stage has two whole blocks
+    *m3 = *m;
+    return true;
+  }
+  const cuuint64_t d3[3] = {(cuuint64_t)kMqKB, rows, K / kMqKB}, s3[2] = {ld, (cuuint64_t)kMqKB};
+  const cuuint32_t b3[3] = {(cuuint32_t)kMqKB, box_rows, (cuuint32_t)kMqBlocks};
+  return enc(m3, 3, d3, s3, b3);
 }
 
 }  // namespace
@@ -518,7 +571,9 @@ dspark_status launch_matmul_q8(const MatmulQ8Call& c) {
     a.tmem_cols = 32;
     while (a.tmem_cols < 2 * a.bn) a.tmem_cols *= 2;
     a.w_bytes = 128 * kMqKB;
-    a.stage_bytes = a.w_bytes + (uint32_t)(a.bn / 2 * kMqKB + 1023) / 1024 * 1024;
+    a.x_bytes = (uint32_t)(a.bn / 2 * kMqKB);
+    a.x_off = kMqBlocks * a.w_bytes;
+    a.stage_bytes = kMqBlocks * (a.w_bytes + a.x_bytes);
     a.stages = (int)std::min<uint32_t>(kPairMaxStages, (kMqSmem - 1024 - misc) / a.stage_bytes);
     a.bars = a.stages * a.stage_bytes;
     box_v = 128;
@@ -534,10 +589,13 @@ dspark_status launch_matmul_q8(const MatmulQ8Call& c) {
     a.nbuf = 2 * a.blocks * a.bn <= 512 ? 2 : 1;
     a.tmem_cols = 32;
     while (a.tmem_cols < a.nbuf * a.blocks * a.bn) a.tmem_cols *= 2;
-    a.w_bytes = (uint32_t)(a.bv * kMqKB + 1023) / 1024 * 1024;
-    a.stage_bytes = a.w_bytes + (uint32_t)(a.bn * kMqKB + 1023) / 1024 * 1024;
+    a.w_bytes = (uint32_t)(a.bv * kMqKB);
+    a.x_bytes = (uint32_t)(a.bn * kMqKB);
+    a.x_off = kMqBlocks * a.w_bytes;
+    a.stage_bytes = kMqBlocks * (a.w_bytes + a.x_bytes);
     // an MMA reads 128 weight rows whatever the tile holds: what follows the last stage is readable
-    const uint32_t slack = (uint32_t)(a.blocks * 16384) > a.stage_bytes ? a.blocks * 16384 - a.stage_bytes : 0;
+    const uint32_t reach = (kMqBlocks - 1) * a.w_bytes + a.blocks * 16384;
+    const uint32_t slack = reach > a.stage_bytes ? reach - a.stage_bytes : 0;
     a.stages = (int)std::min<uint32_t>(kMqMaxStages, (kMqSmem - 1024 - misc - slack) / a.stage_bytes);
     a.bars = a.stages * a.stage_bytes + slack;
     box_v = a.bv;
@@ -545,21 +603,21 @@ dspark_status launch_matmul_q8(const MatmulQ8Call& c) {
     grid = std::min(sms, a.ntiles);
   }
   const size_t smem = 1024 + a.bars + misc;
-  CUtensorMap mW, mX;
-  if (!byte_map(&mW, c.w, c.K, c.N, c.ldw, box_v) || !byte_map(&mX, c.q, c.K, c.M, c.ldq, box_m)) {
+  MqMaps tm;
+  if (!byte_maps(&tm.w, &tm.w3, c.w, c.K, c.N, c.ldw, box_v) || !byte_maps(&tm.x, &tm.x3, c.q, c.K, c.M, c.ldq, box_m)) {
     set_error("dspark_matmul_q8: cuTensorMapEncodeTiled failed");
     return DSPARK_ECUDA;
   }
   cudaError_t rc;
   switch (c.out_dtype) {
     case DSPARK_F32:
-      rc = pair ? launch_pair<DSPARK_F32>(mW, mX, a, grid, smem, c.stream) : launch_mq<DSPARK_F32>(mW, mX, a, grid, smem, c.stream);
+      rc = pair ? launch_pair<DSPARK_F32>(tm, a, grid, smem, c.stream) : launch_mq<DSPARK_F32>(tm, a, grid, smem, c.stream);
       break;
     case DSPARK_BF16:
-      rc = pair ? launch_pair<DSPARK_BF16>(mW, mX, a, grid, smem, c.stream) : launch_mq<DSPARK_BF16>(mW, mX, a, grid, smem, c.stream);
+      rc = pair ? launch_pair<DSPARK_BF16>(tm, a, grid, smem, c.stream) : launch_mq<DSPARK_BF16>(tm, a, grid, smem, c.stream);
       break;
     default:
-      rc = pair ? launch_pair<DSPARK_F16>(mW, mX, a, grid, smem, c.stream) : launch_mq<DSPARK_F16>(mW, mX, a, grid, smem, c.stream);
+      rc = pair ? launch_pair<DSPARK_F16>(tm, a, grid, smem, c.stream) : launch_mq<DSPARK_F16>(tm, a, grid, smem, c.stream);
       break;
   }
   if (rc != cudaSuccess) {
