@@ -478,9 +478,12 @@ def _rows2d(t: torch.Tensor, name: str, dtypes=_DTYPES) -> torch.Tensor:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype not in dtypes:
         raise ValueError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
-    if t.dim() < 2:
+    nd = t.dim()
+    if nd >= 2 and t.is_contiguous():
+        return t if nd == 2 else t.view(-1, t.shape[-1])
+    if nd < 2:
         raise ValueError(f"{name} must have at least 2 dimensions")
-    if t.dim() > 2:
+    if nd > 2:
         try:
             t = t.view(-1, t.shape[-1])
         except RuntimeError as e:
@@ -512,6 +515,10 @@ def _arg(t: Optional[torch.Tensor], name: str, dtype, numel: int, dev) -> Option
     return t.data_ptr()
 
 
+# The current stream's handle of a device, without building a Stream object for each call (3 us)
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
 def _elsewhere(dev, stream) -> bool:
     """The call is not for the current device and its current stream."""
     return stream is not None or dev.index != torch.cuda.current_device()
@@ -541,26 +548,42 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, T: float = 1.0, *
                    top_idx=top_idx, top_logp=top_logp, stats=stats, flags=flags)
     top = int(top)
     N, V = tokens.numel(), l2.shape[1]
-    shape = tuple(tokens.shape)
-    if logp is None:
-        logp = torch.empty(shape, dtype=torch.float32, device=dev)
-    if entropy is None:
-        entropy = torch.empty(shape, dtype=torch.float32, device=dev)
-    if stats is None:
-        stats = torch.empty(shape + (2,), dtype=torch.float32, device=dev)
-    if top > 0:
-        if top_idx is None:
-            top_idx = torch.empty(shape + (top,), dtype=torch.int32, device=dev)
-        if top_logp is None:
-            top_logp = torch.empty(shape + (top,), dtype=torch.float32, device=dev)
-    else:
+    shape = tokens.shape
+    if top <= 0:
         top_idx = top_logp = None
+    if logp is None and entropy is None and stats is None and top_idx is None and top_logp is None:
+        # the outputs share one allocation
+        flat = len(shape) == 1
+        if top > 0:
+            stats, logp, entropy, top_logp, top_idx = torch.empty(
+                N * (4 + 2 * top), dtype=torch.float32, device=dev).split_with_sizes((2 * N, N, N, N * top, N * top))
+            alt = (N, top) if flat else shape + (top,)
+            top_logp, top_idx = top_logp.view(alt), top_idx.view(torch.int32).view(alt)
+        else:
+            stats, logp, entropy = torch.empty(4 * N, dtype=torch.float32, device=dev).split_with_sizes((2 * N, N, N))
+        if flat:
+            stats = stats.view(N, 2)
+        else:
+            stats, logp, entropy = stats.view(shape + (2,)), logp.view(shape), entropy.view(shape)
+        outs = [t.data_ptr() for t in (logp, entropy, top_idx, top_logp, stats) if t is not None]
+        if top <= 0:
+            outs[2:2] = (None, None)
+    else:
+        def new(t, tail, dtype):
+            return torch.empty(shape + tail, dtype=dtype, device=dev) if t is None else t
+
+        logp, entropy = new(logp, (), torch.float32), new(entropy, (), torch.float32)
+        stats = new(stats, (2,), torch.float32)
+        if top > 0:
+            top_idx, top_logp = new(top_idx, (top,), torch.int32), new(top_logp, (top,), torch.float32)
+        outs = [_arg(logp, "logp", torch.float32, N, dev), _arg(entropy, "entropy", torch.float32, N, dev),
+                _arg(top_idx, "top_idx", torch.int32, N * top, dev),
+                _arg(top_logp, "top_logp", torch.float32, N * top, dev),
+                _arg(stats, "stats", torch.float32, 2 * N, dev)]
     st = lib.dspark_token_logprobs(
         l2.data_ptr(), _DTYPES[l2.dtype], _ld(l2), l2.shape[0], _arg(rows, "rows", torch.int64, N, dev),
-        _arg(tokens, "tokens", torch.int32, N, dev), N, V, float(T), top, _arg(logp, "logp", torch.float32, N, dev),
-        _arg(entropy, "entropy", torch.float32, N, dev), _arg(top_idx, "top_idx", torch.int32, N * top, dev),
-        _arg(top_logp, "top_logp", torch.float32, N * top, dev), _arg(stats, "stats", torch.float32, 2 * N, dev),
-        _arg(flags, "flags", torch.int32, N, dev), torch.cuda.current_stream().cuda_stream)
+        _arg(tokens, "tokens", torch.int32, N, dev), N, V, float(T), top, *outs,
+        _arg(flags, "flags", torch.int32, N, dev), _raw_stream(dev.index))
     _check("dspark_token_logprobs", st)
     return logp, entropy, top_idx, top_logp, stats
 
@@ -601,16 +624,28 @@ def token_logprobs_backward(logits: torch.Tensor, tokens: torch.Tensor, T: float
         _arg(stats, "stats", torch.float32, 2 * N, dev), _arg(entropy, "entropy", torch.float32, N, dev),
         _arg(g_logp, "g_logp", torch.float32, N, dev), _arg(g_entropy, "g_entropy", torch.float32, N, dev), top,
         _arg(top_idx, "top_idx", torch.int32, N * top, dev), _arg(g_top, "g_top", torch.float32, N * top, dev),
-        g2.data_ptr(), _ld(g2), torch.cuda.current_stream().cuda_stream)
+        g2.data_ptr(), _ld(g2), _raw_stream(dev.index))
     _check("dspark_token_logprobs_backward", st)
     return grad
 
 
-def _q8_rows(lead, d: int, dev) -> torch.Tensor:
-    """An int8 tensor [*lead, d] whose rows start on 16 bytes (what matmul_q8 reads)."""
-    ld = (d + 15) // 16 * 16
-    q = torch.empty(tuple(lead) + (ld,), dtype=torch.int8, device=dev)
-    return q if ld == d else q[..., :d]
+def _q8_out(x, d: int, M: int, q, scale, dev):
+    """The int8 rows and scales of x's rows, given or new, with their addresses and the row stride.
+    New rows start on 16 bytes (what matmul_q8 reads)."""
+    lead = x.shape[:-1]
+    if q is None:
+        ldq = (d + 15) // 16 * 16
+        q = torch.empty(lead + (ldq,), dtype=torch.int8, device=dev)
+        qp = q.data_ptr()
+        if ldq != d:
+            q = q[..., :d]
+    else:
+        t = _like(q, "q", x, torch.int8)
+        qp, ldq = t.data_ptr(), _ld(t)
+    if scale is None:
+        scale = torch.empty(lead, dtype=torch.float32, device=dev)
+        return q, qp, ldq, scale, scale.data_ptr()
+    return q, qp, ldq, scale, _arg(scale, "scale", torch.float32, M, dev)
 
 
 def _like(t: torch.Tensor, name: str, ref: torch.Tensor, dtype) -> torch.Tensor:
@@ -634,24 +669,26 @@ def rmsnorm_q8(x: torch.Tensor, gain: Optional[torch.Tensor], eps: float, *, res
     if _elsewhere(dev, stream):
         return _at(rmsnorm_q8, dev, stream, x, gain, eps, residual=residual, h_out=h_out, q=q, scale=scale)
     M, d = x2.shape
-    gdt = x2.dtype
+    dt = x2.dtype
+    gdt = dt
     if gain is not None and gain.dtype != gdt:
         gdt = torch.float32
     r2 = h2 = None
     if residual is not None:
-        r2 = _like(residual, "residual", x, x.dtype)
-        h_out = torch.empty(x.shape, dtype=x.dtype, device=dev) if h_out is None else h_out
-        h2 = _like(h_out, "h_out", x, x.dtype)
+        r2 = _like(residual, "residual", x, dt)
+        if h_out is None:
+            h_out = torch.empty(x.shape, dtype=dt, device=dev)
+            h2 = h_out.data_ptr(), d
+        else:
+            t = _like(h_out, "h_out", x, dt)
+            h2 = t.data_ptr(), _ld(t)
     else:
         h_out = None
-    q = _q8_rows(x.shape[:-1], d, dev) if q is None else q
-    q2 = _like(q, "q", x, torch.int8)
-    scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev) if scale is None else scale
+    q, qp, ldq, scale, sp = _q8_out(x, d, M, q, scale, dev)
     st = lib.dspark_rmsnorm_q8(
-        x2.data_ptr(), _DTYPES[x2.dtype], _ld(x2), None if r2 is None else r2.data_ptr(), 0 if r2 is None else _ld(r2),
-        _arg(gain, "gain", gdt, d, dev), _DTYPES[gdt], M, d, float(eps), None if h2 is None else h2.data_ptr(),
-        0 if h2 is None else _ld(h2), q2.data_ptr(), _ld(q2), _arg(scale, "scale", torch.float32, M, dev),
-        torch.cuda.current_stream().cuda_stream)
+        x2.data_ptr(), _DTYPES[dt], _ld(x2), None if r2 is None else r2.data_ptr(), 0 if r2 is None else _ld(r2),
+        _arg(gain, "gain", gdt, d, dev), _DTYPES[gdt], M, d, float(eps), None if h2 is None else h2[0],
+        0 if h2 is None else h2[1], qp, ldq, sp, _raw_stream(dev.index))
     _check("dspark_rmsnorm_q8", st)
     return q, scale, h_out
 
@@ -663,11 +700,8 @@ def quantize_q8(x: torch.Tensor, *, q=None, scale=None, stream=None) -> Tuple[to
     if _elsewhere(dev, stream):
         return _at(quantize_q8, dev, stream, x, q=q, scale=scale)
     M, d = x2.shape
-    q = _q8_rows(x.shape[:-1], d, dev) if q is None else q
-    q2 = _like(q, "q", x, torch.int8)
-    scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev) if scale is None else scale
-    st = lib.dspark_quantize_q8(x2.data_ptr(), _DTYPES[x2.dtype], _ld(x2), M, d, q2.data_ptr(), _ld(q2),
-                                _arg(scale, "scale", torch.float32, M, dev), torch.cuda.current_stream().cuda_stream)
+    q, qp, ldq, scale, sp = _q8_out(x, d, M, q, scale, dev)
+    st = lib.dspark_quantize_q8(x2.data_ptr(), _DTYPES[x2.dtype], _ld(x2), M, d, qp, ldq, sp, _raw_stream(dev.index))
     _check("dspark_quantize_q8", st)
     return q, scale
 
@@ -694,15 +728,15 @@ def matmul_q8(q: torch.Tensor, q_scale: torch.Tensor, w: torch.Tensor, w_scale: 
         if out_dtype not in _DTYPES:
             raise ValueError(f"out_dtype must be fp32, bf16 or fp16, got {out_dtype}")
         out = torch.empty(q.shape[:-1] + (N,), dtype=out_dtype, device=dev)
-        o2 = out.view(-1, N) if out.dim() != 2 else out
+        ldo = N
     else:
-        o2 = _rows2d(out, "out")
+        ldo = _ld(_rows2d(out, "out"))
         if out.device != dev or out.shape != q.shape[:-1] + (N,):
             raise ValueError(f"out must be {tuple(q.shape[:-1]) + (N,)} on {dev}, got {tuple(out.shape)}")
     ldq, ldw = (t.stride(0) if t.shape[0] > 1 else (K + 15) // 16 * 16 for t in (q2, w2))
     st = lib.dspark_matmul_q8(
         q2.data_ptr(), ldq, _arg(q_scale, "q_scale", torch.float32, M, dev), w2.data_ptr(), ldw,
-        _arg(w_scale, "w_scale", torch.float32, N, dev), M, N, K, o2.data_ptr(), _DTYPES[o2.dtype], _ld(o2),
-        _arg(flags, "flags", torch.int32, M, dev), torch.cuda.current_stream().cuda_stream)
+        _arg(w_scale, "w_scale", torch.float32, N, dev), M, N, K, out.data_ptr(), _DTYPES[out.dtype], ldo,
+        _arg(flags, "flags", torch.int32, M, dev), _raw_stream(dev.index))
     _check("dspark_matmul_q8", st)
     return out
