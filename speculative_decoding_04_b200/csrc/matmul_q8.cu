@@ -59,12 +59,26 @@ struct MqMaps {
   CUtensorMap w, x, w3, x3;
 };
 
+// A position in the ring of stages, advanced without divisions: the loops that issue copies and MMAs
+// have a few hundred cycles a stage.
+struct MqRing {
+  int s;
+  uint32_t phase;
+  __device__ __forceinline__ void next(int stages) {
+    if (++s == stages) {
+      s = 0;
+      phase ^= 1u;
+    }
+  }
+};
+
 struct MqSync {
   volatile int* abort;
 };
 
-// Bounded wait shared by all roles; after any timeout every later wait returns at once.
+// Bounded wait shared by all roles; after any timeout every later wait that has to wait returns at once.
 __device__ __forceinline__ bool mq_wait(const MqSync& s, uint64_t* bar, uint32_t parity) {
+  if (mbar_try_wait(bar, parity)) return true;
   if (*s.abort) return false;
   for (uint32_t i = 0; i < kSpinLimit; ++i) {
     if (mbar_try_wait(bar, parity)) return true;
@@ -145,13 +159,14 @@ __global__ void __launch_bounds__(kMqThreads, 1)
 
   if (warp == 0) {
     if (lane == 0) {
+      MqRing r{0, 0};
       int it = 0;
       bool ok = true;
       for (int t = blockIdx.x; ok && t < a.ntiles; t += gridDim.x) {
         const int v0 = (t / a.ntok) * a.bv, m0 = (t % a.ntok) * a.bn;
-        for (int k = 0; k < nkb; k += kMqBlocks, ++it) {
-          const int s = it % a.stages;
-          if (!mq_wait(sy, &empty[s], ((it / a.stages) & 1) ^ 1)) {
+        for (int k = 0; k < nkb; k += kMqBlocks, ++it, r.next(a.stages)) {
+          const int s = r.s;
+          if (!mq_wait(sy, &empty[s], r.phase ^ 1u)) {
             ok = false;
             break;
           }
@@ -180,29 +195,31 @@ __global__ void __launch_bounds__(kMqThreads, 1)
                              | (1u << 7) | (1u << 10)           // A, B signed 8-bit
                              | ((uint32_t)(a.bn >> 3) << 17)    // N
                              | ((uint32_t)(128 >> 4) << 24);    // M
-      int it = 0, n = 0;
+      MqRing r{0, 0}, acc_r{0, 0};
+      const uint64_t desc0 = smem_desc(smem_u32(sm), 16u, 1024u, 2u);  // + bytes / 16 for any stage and block
       bool ok = true;
-      for (int t = blockIdx.x; ok && t < a.ntiles; t += gridDim.x, ++n) {
-        const int buf = n % a.nbuf;
-        if (!mq_wait(sy, &t_empty[buf], ((n / a.nbuf) & 1) ^ 1)) break;
+      for (int t = blockIdx.x; ok && t < a.ntiles; t += gridDim.x, acc_r.next(a.nbuf)) {
+        const int buf = acc_r.s;
+        if (!mq_wait(sy, &t_empty[buf], acc_r.phase ^ 1u)) break;
         tc_fence_after();
         const uint32_t acc = tmem + (uint32_t)(buf * a.blocks * a.bn);
-        for (int k = 0; k < nkb; k += kMqBlocks, ++it) {
-          const int s = it % a.stages;
-          if (!mq_wait(sy, &full[s], (it / a.stages) & 1)) {
+        for (int k = 0; k < nkb; k += kMqBlocks, r.next(a.stages)) {
+          const int s = r.s;
+          if (!mq_wait(sy, &full[s], r.phase)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t st = smem_u32(sm + s * a.stage_bytes);
-          const int nb = min(kMqBlocks, nkb - k);
-          for (int i = 0; i < nb; ++i) {
-            const uint32_t w = st + i * a.w_bytes, x = st + a.x_off + i * a.x_bytes;
+          const uint64_t st = desc0 + ((uint32_t)s * a.stage_bytes >> 4);
+#pragma unroll
+          for (int i = 0; i < kMqBlocks; ++i) {
+            if (k + i >= nkb) break;
+            const uint64_t w = st + (i * a.w_bytes >> 4), x = st + ((a.x_off + i * a.x_bytes) >> 4);
             for (int b = 0; b < a.blocks; ++b)
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk)
-                tc_mma_i8(acc + (uint32_t)(b * a.bn), smem_desc(w + b * 16384u + kk * 32u, 16u, 1024u, 2u),
-                          smem_desc(x + kk * 32u, 16u, 1024u, 2u), idesc, (k | i | kk) != 0 ? 1u : 0u);
+                tc_mma_i8(acc + (uint32_t)(b * a.bn), w + (b * 1024u + kk * 2u), x + kk * 2u, idesc,
+                          (k | i | kk) != 0 ? 1u : 0u);
           }
           tc_commit(&empty[s]);
         }
@@ -373,20 +390,22 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 
   if (warp == 0) {
     if (lane == 0) {
+      MqRing r{0, 0};
       int it = 0;
       bool ok = true;
+      const uint32_t full0 = mapa_rank(smem_u32(full), 0);
       for (int t = pair; ok && t < a.ntiles; t += npairs) {
         const int v0 = (t / a.ntok) * 256 + (int)rank * 128, m0 = (t % a.ntok) * a.bn + (int)rank * half;
-        for (int k = 0; k < nkb; k += kMqBlocks, ++it) {
-          const int s = it % a.stages;
-          if (!mq_wait(sy, &empty[s], ((it / a.stages) & 1) ^ 1)) {
+        for (int k = 0; k < nkb; k += kMqBlocks, ++it, r.next(a.stages)) {
+          const int s = r.s;
+          if (!mq_wait(sy, &empty[s], r.phase ^ 1u)) {
             ok = false;
             break;
           }
           uint8_t* st = sm + s * a.stage_bytes;
           const int nb = min(kMqBlocks, nkb - k);
           if (rank == 0) mbar_arrive_expect_tx(&full[s], (uint32_t)(256 + a.bn) * kMqKB * nb);
-          const uint32_t bar = mapa_rank(smem_u32(&full[s]), 0);
+          const uint32_t bar = full0 + 8u * s;
           if ((k + kMqBlocks) * kMqKB <= a.K) {
             tma_load_3d_pair(st, &tm.w3, 0, v0, k, bar);
             tma_load_3d_pair(st + a.x_off, &tm.x3, 0, m0, k, bar);
@@ -409,28 +428,29 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     if (rank == 0 && lane == 0) {
       const uint32_t idesc = (2u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(a.bn >> 3) << 17) |
                              ((uint32_t)(256 >> 4) << 24);
-      int it = 0, n = 0;
+      MqRing r{0, 0}, acc_r{0, 0};
+      const uint64_t desc0 = smem_desc(smem_u32(sm), 16u, 1024u, 2u);
       bool ok = true;
-      for (int t = pair; ok && t < a.ntiles; t += npairs, ++n) {
-        const int buf = n & 1;
-        if (!mq_wait(sy, &t_empty[buf], ((n >> 1) & 1) ^ 1)) break;
+      for (int t = pair; ok && t < a.ntiles; t += npairs, acc_r.next(2)) {
+        const int buf = acc_r.s;
+        if (!mq_wait(sy, &t_empty[buf], acc_r.phase ^ 1u)) break;
         tc_fence_after();
         const uint32_t acc = tmem + (uint32_t)(buf * a.bn);
-        for (int k = 0; k < nkb; k += kMqBlocks, ++it) {
-          const int s = it % a.stages;
-          if (!mq_wait(sy, &full[s], (it / a.stages) & 1)) {
+        for (int k = 0; k < nkb; k += kMqBlocks, r.next(a.stages)) {
+          const int s = r.s;
+          if (!mq_wait(sy, &full[s], r.phase)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t st = smem_u32(sm + s * a.stage_bytes);
-          const int nb = min(kMqBlocks, nkb - k);
-          for (int i = 0; i < nb; ++i) {
-            const uint32_t w = st + i * a.w_bytes, x = st + a.x_off + i * a.x_bytes;
+          const uint64_t st = desc0 + ((uint32_t)s * a.stage_bytes >> 4);
+#pragma unroll
+          for (int i = 0; i < kMqBlocks; ++i) {
+            if (k + i >= nkb) break;
+            const uint64_t w = st + (i * a.w_bytes >> 4), x = st + ((a.x_off + i * a.x_bytes) >> 4);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              tc_mma_i8_pair(acc, smem_desc(w + kk * 32u, 16u, 1024u, 2u), smem_desc(x + kk * 32u, 16u, 1024u, 2u), idesc,
-                             (k | i | kk) != 0 ? 1u : 0u);
+              tc_mma_i8_pair(acc, w + kk * 2u, x + kk * 2u, idesc, (k | i | kk) != 0 ? 1u : 0u);
           }
           tc_commit_pair(&empty[s]);
         }
@@ -535,14 +555,17 @@ static bool byte_maps(CUtensorMap* m, CUtensorMap* m3, const int8_t* base, uint6
   };
   const cuuint64_t d2[2] = {K, rows}, s2[1] = {ld};
   const cuuint32_t b2[2] = {(cuuint32_t)kMqKB, box_rows};
-  if (!enc(m, 2, d2, s2, b2)) return false;
-  if (K < kMqBlocks * kMqKB) {  // no stage has two whole blocks
+  const bool whole = K % (kMqBlocks * kMqKB) == 0, any = K >= kMqBlocks * kMqKB;
+  if (!whole && !enc(m, 2, d2, s2, b2)) return false;
+  if (!any) {  // no stage has two whole blocks
     *m3 = *m;
     return true;
   }
   const cuuint64_t d3[3] = {(cuuint64_t)kMqKB, rows, K / kMqKB}, s3[2] = {ld, (cuuint64_t)kMqKB};
   const cuuint32_t b3[3] = {(cuuint32_t)kMqKB, box_rows, (cuuint32_t)kMqBlocks};
-  return enc(m3, 3, d3, s3, b3);
+  if (!enc(m3, 3, d3, s3, b3)) return false;
+  if (whole) *m = *m3;  // not used
+  return true;
 }
 
 }  // namespace
