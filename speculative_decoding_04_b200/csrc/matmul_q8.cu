@@ -49,14 +49,17 @@ struct MqArgs {
   int stages, nbuf, blocks, tmem_cols;
   uint32_t w_bytes, x_bytes;            // one block of K: bytes of the tile's weights and tokens
   uint32_t x_off, stage_bytes, bars;    // tokens within a stage; a stage; barriers after the stages
+  uint32_t out_off;                     // (CTA pairs) staging of the output
+  int out_tma;                          // (CTA pairs) the output takes TMA stores
 };
 
 // Tensor maps of the weights and the tokens: [rows, K] with boxes of 128 bytes of K by the tile's rows,
 // and the same matrix as [K / 128][rows][128 bytes] with boxes of two blocks.  One copy of two blocks
-// streams faster than two of one (the copy engine's rate grows with the copy: pairs at 1088 x 151936 x
-// 4096, 684 -> PAIR3D us); the last odd or partial block comes by the first map, which ends at K.
+// streams faster than two of one (1088 x 151936 x 4096: 485 against 530 us, one token 115 against 121);
+// the last odd or partial block comes by the first map, which ends at K.
 struct MqMaps {
   CUtensorMap w, x, w3, x3;
+  CUtensorMap out;  // [M, N] of the output's type in boxes of kOutTokens x 128 (CTA pairs, out_tma)
 };
 
 // A position in the ring of stages, advanced without divisions: the loops that issue copies and MMAs
@@ -282,6 +285,7 @@ __global__ void __launch_bounds__(kMqThreads, 1)
 constexpr int kPairThreads = 384;
 constexpr int kPairEpiWarps = 8;
 constexpr int kPairMaxStages = 8;
+constexpr int kOutTokens = 16;  // tokens of one staged store
 
 __device__ __forceinline__ uint32_t mapa_rank(uint32_t addr, uint32_t rank) {
   uint32_t r;
@@ -324,20 +328,6 @@ __device__ __forceinline__ void tc_commit_pair(uint64_t* bar) {
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
           smem_u32(bar)),
       "h"((uint16_t)3)
-      : "memory");
-}
-
-// 32 lanes x 32 consecutive 32-bit columns (no wait).
-__device__ __forceinline__ void tmem_ld_x32(uint32_t taddr, uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr)
       : "memory");
 }
 
@@ -462,30 +452,60 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       }
     }
   } else if (warp >= 4) {
-    const int q = warp & 3, h = (warp - 4) >> 2;  // lane quadrant; which chunks of 32 columns
-    int n = 0;
-    for (int t = pair; t < a.ntiles; t += npairs, ++n) {
-      const int buf = n & 1;
-      const int v = (t / a.ntok) * 256 + (int)rank * 128 + q * 32 + lane, m0 = (t % a.ntok) * a.bn;
+    // The four warps of a group h hold 128 consecutive outputs of a token on their lanes.  Chunks of 16
+    // tokens alternate between the two groups; a chunk is scaled, staged in shared memory as [16][128]
+    // and written by one TMA store (which also clips it to the matrix), two chunks in flight per group.
+    // Rows that do not take TMA stores (not on 16 bytes) are written from the registers: 32 outputs of
+    // one token a store (4096 x 129280 x 2048 in bf16: 919 us with those stores, 778 staged).
+    constexpr uint32_t kOutBytes = kOutTokens * 128u * (DT == DSPARK_F32 ? 4u : 2u);
+    const int q = warp & 3, h = (warp - 4) >> 2;
+    const bool issuer = q == 0 && lane == 0;
+    int staged = 0;
+    MqRing acc_r{0, 0};
+    for (int t = pair; t < a.ntiles; t += npairs, acc_r.next(2)) {
+      const int buf = acc_r.s;
+      const int v0 = (t / a.ntok) * 256 + (int)rank * 128, v = v0 + q * 32 + lane, m0 = (t % a.ntok) * a.bn;
       const bool mine = v < a.N;
       const float sw = mine ? __ldg(a.w_scale + v) : 0.f;
       const int nm = min(a.bn, a.M - m0);
-      const bool ok = __all_sync(0xffffffffu, mq_wait(sy, &t_full[buf], (n >> 1) & 1));
+      float sq = h * kOutTokens + lane < nm && lane < kOutTokens ? __ldg(a.q_scale + m0 + h * kOutTokens + lane) : 0.f;
+      const bool ok = __all_sync(0xffffffffu, mq_wait(sy, &t_full[buf], acc_r.phase));
       tc_fence_after();
       const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * a.bn);
-      for (int c = h * 32; c < nm; c += 64) {
-        uint32_t r[32];
-        const float sq = c + lane < nm ? __ldg(a.q_scale + m0 + c + lane) : 0.f;
+      for (int c = h * kOutTokens; c < nm; c += 2 * kOutTokens) {
+        uint32_t r[16];
         if (ok) {
-          tmem_ld_x32(acc + c, r);
+          tmem_ld_x16(acc + c, r);
           tmem_wait_ld();
         }
-        long long o = (long long)(m0 + c) * a.ldo + v;
+        const float s_cur = sq;
+        const int cn = c + 2 * kOutTokens + lane;
+        sq = cn < nm && lane < kOutTokens ? __ldg(a.q_scale + m0 + cn) : 0.f;
+        float o[16];
 #pragma unroll
-        for (int j = 0; j < 32; ++j, o += a.ldo) {
-          const float s = __shfl_sync(0xffffffffu, sq, j);
-          if (c + j < nm && mine)
-            store_out<DT>(a.out, o, ok ? (float)(int32_t)r[j] * s * sw : __int_as_float(0x7FC00000));
+        for (int j = 0; j < 16; ++j) {
+          const float s = __shfl_sync(0xffffffffu, s_cur, j);
+          o[j] = ok ? (float)(int32_t)r[j] * s * sw : __int_as_float(0x7FC00000);
+        }
+        if (a.out_tma) {
+          uint8_t* stage = sm + a.out_off + (uint32_t)(h * 2 + (staged & 1)) * kOutBytes;
+          ++staged;
+          if (issuer) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+          named_bar(1 + h, 128);  // the stage's earlier store has read it
+#pragma unroll
+          for (int j = 0; j < 16; ++j) store_out<DT>(stage, j * 128 + q * 32 + lane, o[j]);
+          fence_proxy_async_smem();
+          named_bar(1 + h, 128);
+          if (issuer && v0 < a.N) {
+            asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(&tm.out),
+                         "r"(smem_u32(stage)), "r"(v0), "r"(m0 + c)
+                         : "memory");
+          }
+          if (issuer) bulk_commit();
+        } else if (mine) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            if (c + j < nm) store_out<DT>(a.out, (long long)(m0 + c + j) * a.ldo + v, o[j]);
         }
       }
       if (!ok && a.flags && q == 0 && h == 0)
@@ -494,6 +514,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(mapa_rank(smem_u32(&t_empty[buf]), 0));
     }
+    if (issuer) bulk_wait0();
   }
   __syncwarp();
   tc_fence_before();
@@ -534,9 +555,7 @@ static cudaError_t launch_mq(const MqMaps& tm, const MqArgs& a, int grid, size_t
   return cudaGetLastError();
 }
 
-// The two tensor maps of a [rows, K] byte matrix (128-byte swizzle).
-static bool byte_maps(CUtensorMap* m, CUtensorMap* m3, const int8_t* base, uint64_t K, uint64_t rows, uint64_t ld,
-                      uint32_t box_rows) {
+static PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
   static std::once_flag once;
   std::call_once(once, [] {
@@ -546,6 +565,13 @@ static bool byte_maps(CUtensorMap* m, CUtensorMap* m3, const int8_t* base, uint6
         q == cudaDriverEntryPointSuccess)
       fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
   });
+  return fn;
+}
+
+// The two tensor maps of a [rows, K] byte matrix (128-byte swizzle).
+static bool byte_maps(CUtensorMap* m, CUtensorMap* m3, const int8_t* base, uint64_t K, uint64_t rows, uint64_t ld,
+                      uint32_t box_rows) {
+  auto fn = encode_fn();
   if (!fn) return false;
   auto enc = [&](CUtensorMap* to, int rank, const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box) {
     const cuuint32_t es[3] = {1, 1, 1};
@@ -566,6 +592,18 @@ static bool byte_maps(CUtensorMap* m, CUtensorMap* m3, const int8_t* base, uint6
   if (!enc(m3, 3, d3, s3, b3)) return false;
   if (whole) *m = *m3;  // not used
   return true;
+}
+
+static bool out_map(CUtensorMap* m, void* out, int dtype, uint64_t N, uint64_t M, uint64_t ldo) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const CUtensorMapDataType dt = dtype == DSPARK_F32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                 : dtype == DSPARK_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                        : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  const cuuint64_t dims[2] = {N, M}, strides[1] = {ldo * (dtype == DSPARK_F32 ? 4 : 2)};
+  const cuuint32_t box[2] = {128, (cuuint32_t)kOutTokens}, es[2] = {1, 1};
+  return fn(m, dt, 2, out, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+            CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace
@@ -597,8 +635,12 @@ dspark_status launch_matmul_q8(const MatmulQ8Call& c) {
     a.x_bytes = (uint32_t)(a.bn / 2 * kMqKB);
     a.x_off = kMqBlocks * a.w_bytes;
     a.stage_bytes = kMqBlocks * (a.w_bytes + a.x_bytes);
-    a.stages = (int)std::min<uint32_t>(kPairMaxStages, (kMqSmem - 1024 - misc) / a.stage_bytes);
-    a.bars = a.stages * a.stage_bytes;
+    const int es = c.out_dtype == DSPARK_F32 ? 4 : 2;
+    const uint32_t staging = 4u * kOutTokens * 128u * es;
+    a.stages = (int)std::min<uint32_t>(kPairMaxStages, (kMqSmem - 1024 - misc - staging) / a.stage_bytes);
+    a.out_off = a.stages * a.stage_bytes;
+    a.bars = a.out_off + staging;
+    a.out_tma = (uintptr_t)c.out % 16 == 0 && c.ldo * es % 16 == 0 && c.ldo * es < (1ll << 40);
     box_v = 128;
     box_m = a.bn / 2;
     grid = 2 * std::min(sms / 2, a.ntiles);
@@ -626,7 +668,11 @@ dspark_status launch_matmul_q8(const MatmulQ8Call& c) {
     grid = std::min(sms, a.ntiles);
   }
   const size_t smem = 1024 + a.bars + misc;
-  MqMaps tm;
+  MqMaps tm{};
+  if (pair && a.out_tma && !out_map(&tm.out, c.out, c.out_dtype, c.N, c.M, c.ldo)) {
+    set_error("dspark_matmul_q8: cuTensorMapEncodeTiled failed for the output");
+    return DSPARK_ECUDA;
+  }
   if (!byte_maps(&tm.w, &tm.w3, c.w, c.K, c.N, c.ldw, box_v) || !byte_maps(&tm.x, &tm.x3, c.q, c.K, c.M, c.ldq, box_m)) {
     set_error("dspark_matmul_q8: cuTensorMapEncodeTiled failed");
     return DSPARK_ECUDA;
