@@ -35,7 +35,7 @@ constexpr int kMqKB = 128;    // bytes (= values) of a block of K: one swizzled 
 constexpr int kMqBlocks = 2;  // blocks of K per stage
 constexpr int kMqMaxStages = 8;
 constexpr uint32_t kMqSmem = 227u * 1024u;
-constexpr int kPairMinTokens = 128;  // more tokens than this: CTA pairs
+constexpr int kMqMaxTokens = 128;      // tokens of one single-CTA call; more than this: CTA pairs
 
 struct MqArgs {
   const float* q_scale;
@@ -214,9 +214,7 @@ __global__ void __launch_bounds__(kMqThreads, 1)
           }
           tc_fence_after();
           const uint64_t st = desc0 + ((uint32_t)s * a.stage_bytes >> 4);
-#pragma unroll
-          for (int i = 0; i < kMqBlocks; ++i) {
-            if (k + i >= nkb) break;
+          for (int i = 0; i < kMqBlocks && k + i < nkb; ++i) {
             const uint64_t w = st + (i * a.w_bytes >> 4), x = st + ((a.x_off + i * a.x_bytes) >> 4);
             for (int b = 0; b < a.blocks; ++b)
 #pragma unroll
@@ -235,30 +233,37 @@ __global__ void __launch_bounds__(kMqThreads, 1)
     }
   } else if (warp >= 4) {
     const int q = warp & 3, b = (warp - 4) >> 2;
-    int n = 0;
-    for (int t = blockIdx.x; t < a.ntiles; t += gridDim.x, ++n) {
-      const int buf = n % a.nbuf;
+    MqRing acc_r{0, 0};
+    for (int t = blockIdx.x; t < a.ntiles; t += gridDim.x, acc_r.next(a.nbuf)) {
+      const int buf = acc_r.s;
       const int v = (t / a.ntok) * a.bv + b * 128 + q * 32 + lane, m0 = (t % a.ntok) * a.bn;
       const bool mine = b < a.blocks && b * 128 + q * 32 + lane < a.bv && v < a.N;
-      const float sw = mine ? __ldg(a.w_scale + v) : 0.f;
       const int nm = min(a.bn, a.M - m0);
-      const bool ok = __all_sync(0xffffffffu, mq_wait(sy, &t_full[buf], (n / a.nbuf) & 1));
+      // both scales before the wait: lane i holds the tokens' i, i + 32, ...
+      const float sw = mine ? __ldg(a.w_scale + v) : 0.f;
+      float sq[kMqMaxTokens / 32];
+#pragma unroll
+      for (int i = 0; i < kMqMaxTokens / 32; ++i) sq[i] = i * 32 + lane < nm ? __ldg(a.q_scale + m0 + i * 32 + lane) : 0.f;
+      const bool ok = __all_sync(0xffffffffu, mq_wait(sy, &t_full[buf], acc_r.phase));
       tc_fence_after();
       if (b < a.blocks) {
         const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)((buf * a.blocks + b) * a.bn);
-        for (int c = 0; c < nm; c += 16) {
+#pragma unroll
+        for (int i = 0; i < kMqMaxTokens / 16; ++i) {
+          const int c = i * 16;
+          if (c >= nm) break;
           uint32_t r[16];
           if (ok) {
             tmem_ld_x16(acc + c, r);
             tmem_wait_ld();
           }
+          long long o = (long long)(m0 + c) * a.ldo + v;
 #pragma unroll
-          for (int j = 0; j < 16; ++j)
-            if (c + j < nm && mine) {
-              const int m = m0 + c + j;
-              const float o = ok ? (float)(int32_t)r[j] * __ldg(a.q_scale + m) * sw : __int_as_float(0x7FC00000);
-              store_out<DT>(a.out, (long long)m * a.ldo + v, o);
-            }
+          for (int j = 0; j < 16; ++j, o += a.ldo) {
+            const float s = __shfl_sync(0xffffffffu, sq[i / 2], (c + j) & 31);
+            if (c + j < nm && mine)
+              store_out<DT>(a.out, o, ok ? (float)(int32_t)r[j] * s * sw : __int_as_float(0x7FC00000));
+          }
         }
         if (!ok && a.flags && q == 0 && b == 0)
           for (int m = m0 + lane; m < m0 + nm; m += 32) atomicOr(a.flags + m, DSPARK_FLAG_DEVICE_TIMEOUT);
@@ -620,7 +625,7 @@ dspark_status launch_matmul_q8(const MatmulQ8Call& c) {
   a.M = c.M;
   a.N = c.N;
   a.K = c.K;
-  const bool pair = c.M > kPairMinTokens;
+  const bool pair = c.M > kMqMaxTokens;
   const uint32_t misc = 8 * (2 * kMqMaxStages + 5) + 16;
   const int step = pair ? 32 : 16;
   a.ntok = (c.M + 255) / 256;
@@ -646,8 +651,9 @@ dspark_status launch_matmul_q8(const MatmulQ8Call& c) {
     grid = 2 * std::min(sms / 2, a.ntiles);
   } else {
     // weight rows per tile: the largest tile that gives every CTA the same number of tiles
-    const int per = std::max(1, (int)(((long long)c.N * a.ntok + 256ll * sms - 1) / (256ll * sms)));
-    long long rows = ((long long)c.N * a.ntok + (long long)sms * per - 1) / ((long long)sms * per);
+    // (one token, 151936 x 4096: 115 us; at most 128 rows of 2 or 4 blocks of K 123 and 119, 64 of 8 137)
+    const int per = std::max(1, (int)((c.N + 256ll * sms - 1) / (256ll * sms)));
+    const long long rows = (c.N + (long long)sms * per - 1) / ((long long)sms * per);
     a.bv = (int)std::min(256ll, std::max(16ll, (rows + 15) / 16 * 16));
     a.ntiles = a.ntok * ((c.N + a.bv - 1) / a.bv);
     a.blocks = a.bv > 128 ? 2 : 1;
