@@ -227,8 +227,31 @@ __device__ __forceinline__ CtaPart join_parts(CtaPart p, float c) {
   return CtaPart{warp_sum_f(S), warp_sum_f(E), M, __any_sync(0xffffffffu, p.bad)};
 }
 
+__device__ __forceinline__ uint32_t cluster_addr(const void* p, int rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+  return r;
+}
+
+// Where a tile's maximum goes: this CTA's record, or (clusters) the record of every CTA, lane r writing
+// to CTA r.
+template <bool CLUSTER>
+struct MaxOut {
+  float* own;
+  uint32_t at;
+  bool mine;
+  __device__ MaxOut(float* s_max, int C, int lane) : own(s_max), at(0), mine(lane < (CLUSTER ? C : 1)) {
+    if (CLUSTER && mine) at = cluster_addr(s_max, lane);
+  }
+  __device__ __forceinline__ void put(int t, float m) const {
+    if (!mine) return;
+    if (CLUSTER) asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at + 4u * t), "f"(m) : "memory");
+    else own[t] = m;
+  }
+};
+
 // A warp's running sums over the tiles it takes.
-template <int DT>
+template <int DT, bool CLUSTER>
 struct WarpSums {
   using E = Elem<DT>;
   static constexpr int kPairs = E::kVec / 2, kLoads = RowTiles<DT>::kLoads;
@@ -242,7 +265,7 @@ struct WarpSums {
   // One tile into the sums; false if they are no longer numbers.  Masked values (0 * -inf in E) and NaN
   // need CLAMP; rows without them, most, go without its two instructions a pair.
   template <bool CLAMP>
-  __device__ __forceinline__ bool tile(const uint4 (&v)[kLoads], int lane, float* max_out) {
+  __device__ __forceinline__ bool tile(const uint4 (&v)[kLoads], int t, const MaxOut<CLUSTER>& out) {
     float m = -INFINITY;
 #pragma unroll
     for (int j = 0; j < kLoads; ++j)
@@ -252,7 +275,7 @@ struct WarpSums {
         m = max3_nan(m, x.x, x.y);
       }
     m = warp_max_nan(m);
-    if (lane == 0) *max_out = m;
+    out.put(t, m);
     if (CLAMP) bad |= !(m < INFINITY);  // NaN or +inf
     if (m > R) {                        // the same for all lanes
       const float dr = fmaxf((R - m) * c, kFloor), f = ex2(dr);  // R = -inf: S = E = 0 stay
@@ -279,7 +302,7 @@ struct WarpSums {
 
   // Full tiles t, t + W, ... below end, the next kAhead tiles' loads in flight; false as tile().
   template <bool CLAMP, int W>
-  __device__ __forceinline__ bool pass(const RowTiles<DT>& tiles, int t, int end, int lane, float* max_out) {
+  __device__ __forceinline__ bool pass(const RowTiles<DT>& tiles, int t, int end, int lane, const MaxOut<CLUSTER>& out) {
     const uint4* src = reinterpret_cast<const uint4*>(tiles.p + tiles.start(t)) + lane;
     uint4 buf[kAhead + 1][kLoads];
 #pragma unroll
@@ -289,7 +312,7 @@ struct WarpSums {
       for (int u = 0; u <= kAhead; ++u)
         if (t + u * W < end) {
           fetch<W>(src, u + kAhead, t, end, buf[(u + kAhead) % (kAhead + 1)]);
-          if (!tile<CLAMP>(buf[u], lane, max_out + t + u * W)) return false;
+          if (!tile<CLAMP>(buf[u], t + u * W, out)) return false;
         }
       t += (kAhead + 1) * W;
       src += (kAhead + 1) * (W * 32 * kLoads);
@@ -305,30 +328,26 @@ struct WarpSums {
   }
 };
 
-template <int DT, int W>
+template <int DT, int W, bool CLUSTER>
 __global__ void __launch_bounds__(W * 32, 32 / W) token_logprobs_kernel(LpArgs a) {
   using E = Elem<DT>;
   using T = typename E::T;
   constexpr int kLoads = RowTiles<DT>::kLoads;
   constexpr int kLpWarps = W, kLpThreads = W * 32;
-  // [top^2] candidates found by this CTA, the same again for the whole cluster's (C > 1), and the
-  // maxima of the row's tiles (all CTAs')
+  // [top^2] candidates (rank 0 of a cluster: the whole cluster's), the maxima of the row's tiles
   extern __shared__ __align__(16) uint8_t s_dyn[];
-  const int ncand = a.top * a.top;
   uint64_t* s_cand = reinterpret_cast<uint64_t*>(s_dyn);
+  float* s_max = reinterpret_cast<float*>(s_cand + a.top * a.top);
   __shared__ uint64_t s_top[DSPARK_TOP_MAX];
   __shared__ CtaPart s_warp[kLpWarps];
+  __shared__ CtaPart s_part[kLpMaxCluster];  // (rank 0) the CTAs' sums
   __shared__ int s_sel[DSPARK_TOP_MAX];
-  __shared__ CtaPart s_part;
   __shared__ float s_thr;
-  __shared__ int s_nsel, s_ncand, s_nall;
+  __shared__ int s_nsel, s_ncand;
   __shared__ double s_m, s_logS;
 
   cg::cluster_group cluster = cg::this_cluster();
-  const int C = (int)cluster.num_blocks();
-  uint64_t* s_all = s_cand + ncand;
-  float* s_max = reinterpret_cast<float*>(s_cand + (C > 1 ? 2 : 1) * ncand);
-  const int rank = (int)cluster.block_rank();
+  const int C = CLUSTER ? (int)cluster.num_blocks() : 1, rank = CLUSTER ? (int)cluster.block_rank() : 0;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const long long n = blockIdx.x / C;
   const int tok = __ldg(a.tokens + n);
@@ -354,15 +373,23 @@ __global__ void __launch_bounds__(W * 32, 32 / W) token_logprobs_kernel(LpArgs a
 
   const RowTiles<DT> tiles(static_cast<const T*>(a.logits) + row * a.ld, a.V);
   const int nt = tiles.n;
+  if (tid == 0) s_ncand = 0;
+  // the peers have started before anything is written to them (waited for below)
+  if (CLUSTER) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  const bool in_range = (unsigned)tok < (unsigned)a.V;
+  float x_tok = 0.f;
+  if (rank == 0 && tid == 0 && in_range) x_tok = E::get(tiles.p[tok]);
   const int t0 = (int)((long long)nt * rank / C), t1 = (int)((long long)nt * (rank + 1) / C);
 
   // ---------------------------------------------------------------- one pass over the CTA's tiles
   // full tiles [b0, b1) of the CTA first, then what the row begins or ends with
   const int b0 = max(t0, tiles.head > 0 ? 1 : 0), b1 = min(t1, tiles.full_end());
-  WarpSums<DT> sums(a.c);
-  if (!sums.template pass<false, W>(tiles, b0 + warp, b1, lane, s_max)) {
-    sums = WarpSums<DT>(a.c);
-    sums.template pass<true, W>(tiles, b0 + warp, b1, lane, s_max);
+  if (CLUSTER) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  const MaxOut<CLUSTER> out(s_max, C, lane);
+  WarpSums<DT, CLUSTER> sums(a.c);
+  if (!sums.template pass<false, W>(tiles, b0 + warp, b1, lane, out)) {
+    sums = WarpSums<DT, CLUSTER>(a.c);
+    sums.template pass<true, W>(tiles, b0 + warp, b1, lane, out);
   }
   if (warp == W - 1) {
     for (int e = 0; e < 2; ++e) {
@@ -370,33 +397,25 @@ __global__ void __launch_bounds__(W * 32, 32 / W) token_logprobs_kernel(LpArgs a
       if (t < t0 || t >= t1 || (t >= b0 && t < b1) || (e == 1 && nt == 1)) continue;
       uint4 v[kLoads];
       tiles.load_edge(tiles.start(t), tiles.end(t) - tiles.start(t), lane, v);
-      sums.template tile<true>(v, lane, s_max + t);
+      sums.template tile<true>(v, t, out);
     }
   }
   {
     const float S = warp_sum_f(sums.S2.x + sums.S2.y), Es = warp_sum_f(sums.E2.x + sums.E2.y);
     if (lane == 0) s_warp[warp] = CtaPart{S, Es, sums.R, sums.bad};
   }
-  if (tid == 0) s_ncand = s_nall = 0;
-  __syncthreads();
+  __syncwarp();
+  // the tiles' maxima are everywhere, and the CTA's partial sums here
+  if (CLUSTER) cluster.sync();
+  else __syncthreads();
   if (warp == 1) {
     const CtaPart p = join_parts(lane < kLpWarps ? s_warp[lane] : CtaPart{0.f, 0.f, -INFINITY, 0}, a.c);
-    if (lane == 0) s_part = p;
+    if (lane == 0) *(CLUSTER ? cluster.map_shared_rank(&s_part[rank], 0) : &s_part[0]) = p;
   }
 
   if (a.top > 0) {
     // -------------------------------------------------------------- the row's best tiles
-    if (C > 1) {  // every CTA takes the others' maxima and makes the same choice
-      cluster.sync();
-      for (int t = tid; t < nt; t += kLpThreads)
-        if (t < t0 || t >= t1) {
-          // the CTA whose range holds t
-          int r = (int)(((long long)t * C) / nt);
-          while ((int)((long long)nt * (r + 1) / C) <= t) ++r;
-          s_max[t] = *cluster.map_shared_rank(s_max + t, r);
-        }
-      cluster.sync();  // (also a block barrier) nobody changes its maxima before all have them
-    }
+    // (every CTA of a cluster makes the same choice)
     if (warp == 0) {
       int nsel = 0;
       float last = -INFINITY, best;
@@ -434,6 +453,8 @@ __global__ void __launch_bounds__(W * 32, 32 / W) token_logprobs_kernel(LpArgs a
     // -------------------------------------------------------------- their candidates
     const int nsel = s_nsel;
     const float thr = s_thr;
+    uint64_t* cand = CLUSTER ? cluster.map_shared_rank(s_cand, 0) : s_cand;
+    int* ncand = CLUSTER ? cluster.map_shared_rank(&s_ncand, 0) : &s_ncand;
     for (int j = warp * C + rank; j < nsel; j += kLpWarps * C) {
       const int t = s_sel[j], ts = tiles.start(t);
       uint4 v[kLoads];
@@ -450,10 +471,10 @@ __global__ void __launch_bounds__(W * 32, 32 / W) token_logprobs_kernel(LpArgs a
       const int all = __reduce_add_sync(0xffffffffu, __popc(in));
       if (all <= a.top) {
         if (in) {
-          int at = atomicAdd(&s_ncand, __popc(in));
+          int at = atomicAdd(ncand, __popc(in));
 #pragma unroll
           for (int q = 0; q < kLoads * E::kVec; ++q)
-            if (in >> q & 1) s_cand[at++] = cand_key(value(q), (uint32_t)(ts + index(q)));
+            if (in >> q & 1) cand[at++] = cand_key(value(q), (uint32_t)(ts + index(q)));
         }
       } else {  // more than `top`: take the best ones in turn
         for (int round = 0; round < a.top; ++round) {
@@ -468,7 +489,7 @@ __global__ void __launch_bounds__(W * 32, 32 / W) token_logprobs_kernel(LpArgs a
           const float M = redux_max(best);
           const int bi = bq < 0 ? 0x7FFFFFFF : index(bq);
           const int w = (int)__reduce_min_sync(0xffffffffu, best == M ? (unsigned)bi : 0x7FFFFFFFu);
-          if (lane == 0) s_cand[atomicAdd(&s_ncand, 1)] = cand_key(M, (uint32_t)(ts + w));
+          if (lane == 0) cand[atomicAdd(ncand, 1)] = cand_key(M, (uint32_t)(ts + w));
           if (bi == w) in &= ~(1u << bq);
         }
       }
@@ -476,15 +497,14 @@ __global__ void __launch_bounds__(W * 32, 32 / W) token_logprobs_kernel(LpArgs a
   }
 
   // ---------------------------------------------------------------- join the cluster, write the row
-  if (C > 1) cluster.sync();
+  __syncwarp();
+  if (CLUSTER) cluster.sync();  // the last access to another CTA's memory was before it
   else __syncthreads();
   if (rank == 0) {
     if (warp == 0) {
-      CtaPart p{0.f, 0.f, -INFINITY, 0};
-      if (lane < C) p = C > 1 ? *cluster.map_shared_rank(&s_part, lane) : s_part;
-      if (C > 1) p = join_parts(p, a.c);
+      CtaPart p = s_part[0];
+      if (CLUSTER) p = join_parts(lane < C ? s_part[lane] : CtaPart{0.f, 0.f, -INFINITY, 0}, a.c);
       if (lane == 0) {
-        p = C > 1 ? p : s_part;
         const float nan = __int_as_float(0x7FC00000);
         double logS = log((double)p.S);
         float lp, H, m = p.R;
@@ -502,11 +522,11 @@ __global__ void __launch_bounds__(W * 32, 32 / W) token_logprobs_kernel(LpArgs a
           H = (float)(logS - (double)p.E / (double)p.S * kLn2D);
           lp = 0.f;
         }
-        if ((unsigned)tok >= (unsigned)a.V) {
+        if (!in_range) {
           fl |= DSPARK_FLAG_TOKEN_RANGE;
           lp = nan;
         } else if (!p.bad && p.R > -INFINITY) {
-          lp = (float)(((double)E::get(tiles.p[tok]) - (double)p.R) * a.inv_T - logS);
+          lp = (float)(((double)x_tok - (double)p.R) * a.inv_T - logS);
         }
         a.logp[n] = lp;
         if (a.entropy) a.entropy[n] = H;
@@ -517,26 +537,12 @@ __global__ void __launch_bounds__(W * 32, 32 / W) token_logprobs_kernel(LpArgs a
       }
     }
     if (a.top > 0) {
-      const uint64_t* from = s_cand;
-      int nc = s_ncand;
-      if (C > 1) {
-        for (int r = warp; r < C; r += kLpWarps) {
-          const int k = *cluster.map_shared_rank(&s_ncand, r);
-          const uint64_t* src = cluster.map_shared_rank(s_cand, r);
-          int at = 0;
-          if (lane == 0 && k) at = atomicAdd(&s_nall, k);
-          at = __shfl_sync(0xffffffffu, at, 0);
-          for (int i = lane; i < k; i += 32) s_all[at + i] = src[i];
-        }
-        __syncthreads();
-        from = s_all;
-        nc = s_nall;
-      }
+      const int nc = s_ncand;
       // rank by counting (the keys are distinct): key i goes to place #{j : key j > key i}
       for (int i = tid; i < nc; i += kLpThreads) {
-        const uint64_t k = from[i];
+        const uint64_t k = s_cand[i];
         int place = 0;
-        for (int j = 0; j < nc; ++j) place += from[j] > k;
+        for (int j = 0; j < nc; ++j) place += s_cand[j] > k;
         if (place < a.top) s_top[place] = k;
       }
       __syncthreads();
@@ -551,7 +557,6 @@ __global__ void __launch_bounds__(W * 32, 32 / W) token_logprobs_kernel(LpArgs a
       }
     }
   }
-  if (C > 1) cluster.sync();  // no CTA leaves while rank 0 may still read its shared memory
 }
 
 // ============================================================================ backward
@@ -694,10 +699,10 @@ __global__ void __launch_bounds__(kLbThreads) token_logprobs_bwd_kernel(LbArgs a
 
 // ============================================================================ host
 
-template <int DT, int W>
+template <int DT, int W, bool CLUSTER>
 static cudaError_t launch_lp(const LpArgs& a, int N, int C, int nt, cudaStream_t st) {
-  auto kern = token_logprobs_kernel<DT, W>;
-  const size_t smem = (size_t)(C > 1 ? 2 : 1) * a.top * a.top * 8 + (size_t)nt * 4;
+  auto kern = token_logprobs_kernel<DT, W, CLUSTER>;
+  const size_t smem = (size_t)a.top * a.top * 8 + (size_t)nt * 4;
   cudaError_t rc = ensure_smem_attr((const void*)kern, smem);
   if (rc == cudaSuccess && C > 8) rc = ensure_nonportable_cluster((const void*)kern);
   if (rc != cudaSuccess) return rc;
@@ -726,10 +731,11 @@ static dspark_status launch_lp(const LogprobsCall& c) {
   while (C < kLpMaxCluster && (long long)c.N * 2 * C <= slots && nt / (2 * C) >= 16) C *= 2;
   LpArgs a{c.logits, c.ld, c.rows, c.n_rows, c.tokens, c.V, c.top, 1.0 / (double)c.T, (float)(1.0 / (kLn2D * (double)c.T)),
            c.logp, c.entropy, c.top_idx, c.top_logp, reinterpret_cast<float2*>(c.stats), c.flags};
-  cudaError_t rc = C > 1 ? launch_lp<DT, 16>(a, c.N, C, (int)nt, c.stream) : launch_lp<DT, 8>(a, c.N, C, (int)nt, c.stream);
+  cudaError_t rc = C > 1 ? launch_lp<DT, 16, true>(a, c.N, C, (int)nt, c.stream)
+                         : launch_lp<DT, 8, false>(a, c.N, C, (int)nt, c.stream);
   if (rc != cudaSuccess && C > 8) {  // no clusters of 16 here
     cudaGetLastError();
-    rc = launch_lp<DT, 16>(a, c.N, 8, (int)nt, c.stream);
+    rc = launch_lp<DT, 16, true>(a, c.N, 8, (int)nt, c.stream);
   }
   if (rc != cudaSuccess) {
     cudaGetLastError();
