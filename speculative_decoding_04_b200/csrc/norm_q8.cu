@@ -8,7 +8,10 @@
 //
 // One CTA per row.  The row stays in registers between the pass that reads it (sum of squares and
 // maximum in one block reduction) and the pass that writes q, so every byte moves once; rows too long
-// or not aligned for that are read again from the stored h.  Bound by HBM.
+// or not aligned for that are read again from the stored h.  Bound by HBM: 16384 rows of 5120 bf16 with a
+// residual take 92 us (6.4 TB/s).  What it took to get there is few instructions: with one value at a
+// time the same launch shape measured 127 us, three quarters of its issue slots busy.  A persistent grid
+// that loads a row ahead measured 207 us (the registers of two rows leave too few warps).
 
 #include <cuda_fp16.h>
 
@@ -34,33 +37,78 @@ struct NqArgs {
   float eps;
 };
 
+// 16 bytes of a row: kPairs pairs of values.  add() is x + r rounded to the type: the 16-bit sums are
+// the fp32 sums rounded (a sum that fp32 cannot hold is nowhere near a tie of the 16-bit type).
 template <int DT>
 struct Io;
 template <>
 struct Io<DSPARK_F32> {
   using T = float;
-  static constexpr int kVec = 4;
+  static constexpr int kPairs = 2;
   __device__ static float get(T v) { return v; }
   __device__ static T put(float v) { return v; }
+  __device__ static float2 pair(const uint4& u, int i) {
+    return i == 0 ? make_float2(__uint_as_float(u.x), __uint_as_float(u.y))
+                  : make_float2(__uint_as_float(u.z), __uint_as_float(u.w));
+  }
+  __device__ static uint4 add(const uint4& x, const uint4& r) {
+    const float2 a = p_add(pair(x, 0), pair(r, 0)), b = p_add(pair(x, 1), pair(r, 1));
+    return make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x), __float_as_uint(b.y));
+  }
 };
+__device__ __forceinline__ uint32_t word(const uint4& u, int i) { return i == 0 ? u.x : (i == 1 ? u.y : (i == 2 ? u.z : u.w)); }
 template <>
 struct Io<DSPARK_BF16> {
   using T = __nv_bfloat16;
-  static constexpr int kVec = 8;
+  static constexpr int kPairs = 4;
   __device__ static float get(T v) { return __bfloat162float(v); }
   __device__ static T put(float v) { return __float2bfloat16_rn(v); }
+  __device__ static float2 pair(const uint4& u, int i) {
+    return make_float2(__uint_as_float(word(u, i) << 16), __uint_as_float(word(u, i) & 0xFFFF0000u));
+  }
+  __device__ static uint32_t add2(uint32_t x, uint32_t r) {
+    uint32_t d;
+    asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(x), "r"(r));
+    return d;
+  }
+  __device__ static uint4 add(const uint4& x, const uint4& r) {
+    return make_uint4(add2(x.x, r.x), add2(x.y, r.y), add2(x.z, r.z), add2(x.w, r.w));
+  }
 };
 template <>
 struct Io<DSPARK_F16> {
   using T = __half;
-  static constexpr int kVec = 8;
+  static constexpr int kPairs = 4;
   __device__ static float get(T v) { return __half2float(v); }
   __device__ static T put(float v) { return __float2half_rn(v); }
+  __device__ static float2 pair(const uint4& u, int i) {
+    const uint32_t w = word(u, i);
+    return __half22float2(*reinterpret_cast<const __half2*>(&w));
+  }
+  __device__ static uint32_t add2(uint32_t x, uint32_t r) {
+    uint32_t d;
+    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(x), "r"(r));
+    return d;
+  }
+  __device__ static uint4 add(const uint4& x, const uint4& r) {
+    return make_uint4(add2(x.x, r.x), add2(x.y, r.y), add2(x.z, r.z), add2(x.w, r.w));
+  }
 };
 
-template <typename T, int N>
-struct alignas(sizeof(T) * N) Pack {
-  T v[N];
+// Gains of a 16-byte vector's values, as loaded: fp32, or the row's type.
+template <int DT, bool GF32>
+struct Gain {
+  static constexpr int kWords = GF32 ? Io<DT>::kPairs / 2 : 1;
+  uint4 w[kWords];
+  __device__ __forceinline__ void load(const void* gain, int i) {
+    if (!gain) return;
+#pragma unroll
+    for (int k = 0; k < kWords; ++k) w[k] = __ldg(static_cast<const uint4*>(gain) + i * kWords + k);
+  }
+  __device__ __forceinline__ float2 pair(bool have, int i) const {
+    if (!have) return make_float2(1.f, 1.f);
+    return GF32 ? Io<DSPARK_F32>::pair(w[i / 2], i % 2) : Io<DT>::pair(w[0], i);
+  }
 };
 
 __device__ __forceinline__ float nq_max_nan(float a, float b) {
@@ -73,8 +121,7 @@ __device__ __forceinline__ float nq_max_nan(float a, float b) {
 __device__ __forceinline__ float2 block_sum_max(float s, float m, float* sh) {
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, nw = (blockDim.x + 31) >> 5;
   s = warp_sum_f(s);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = nq_max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+  m = warp_max_nan(m);
   if (nw == 1) return make_float2(s, m);
   __syncthreads();  // sh may hold an earlier result
   if (lane == 0) {
@@ -84,10 +131,7 @@ __device__ __forceinline__ float2 block_sum_max(float s, float m, float* sh) {
   __syncthreads();
   s = lane < nw ? sh[lane] : 0.f;
   m = lane < nw ? sh[32 + lane] : 0.f;
-  s = warp_sum_f(s);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = nq_max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
-  return make_float2(s, m);
+  return make_float2(warp_sum_f(s), warp_max_nan(m));
 }
 
 // The row's scale and the factor that takes v to the 8-bit grid.  Rows whose maximum is below 2^-120
@@ -106,86 +150,97 @@ __device__ __forceinline__ int8_t to_q8(float v, float f) { return (int8_t)__flo
 
 constexpr float kTiny = 0x1p-70f;
 
+// Two products v f (each rounded) to the nearest integers, ties to even: adding 1.5 * 2^23 leaves the
+// integer in the low bits of the sum.  (Scalar instructions: a packed product followed by a packed
+// addition was seen to round once, and the grid is defined on the rounded product.)
+__device__ __forceinline__ float2 to_grid(float2 v, float f) {
+  const float2 t = make_float2(__fmul_rn(v.x, f), __fmul_rn(v.y, f));
+  return make_float2(__fadd_rn(t.x, 12582912.f), __fadd_rn(t.y, 12582912.f));
+}
+__device__ __forceinline__ uint32_t low_bytes(float2 a, float2 b) {
+  const uint32_t lo = __byte_perm(__float_as_uint(a.x), __float_as_uint(a.y), 0x0040);
+  const uint32_t hi = __byte_perm(__float_as_uint(b.x), __float_as_uint(b.y), 0x0040);
+  return __byte_perm(lo, hi, 0x5410);
+}
+
+// VPT vectors of 16 bytes a thread.  The row waits in its stored type and v is formed again for its
+// second use: fewer registers, more CTAs, more loads in flight.
 template <int DT, bool GF32, int VPT>
-__global__ void __launch_bounds__(1024) rmsnorm_q8_reg(NqArgs a) {
+__global__ void __launch_bounds__(VPT == 1 ? 256 : VPT == 2 ? 512 : 1024) rmsnorm_q8_reg(NqArgs a) {
   using I = Io<DT>;
   using T = typename I::T;
-  constexpr int kVec = I::kVec;
-  using P = Pack<T, kVec>;
-  using Q = Pack<int8_t, kVec>;
-  using G = Pack<float, 4>;
   __shared__ float sh[64];
   const long long row = blockIdx.x;
-  const int nv = a.d / kVec;
-  const P* x = reinterpret_cast<const P*>(static_cast<const T*>(a.x) + row * a.ldx);
-  const P* res = a.res ? reinterpret_cast<const P*>(static_cast<const T*>(a.res) + row * a.ldr) : nullptr;
-  P xv[VPT], rv[VPT];
+  const int nv = a.d / (2 * I::kPairs);
+  const bool have_g = a.gain != nullptr;
+  const uint4* x = reinterpret_cast<const uint4*>(static_cast<const T*>(a.x) + row * a.ldx);
+  uint4 hv[VPT];
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
     const int i = j * blockDim.x + threadIdx.x;
-    if (i < nv) xv[j] = x[i];
-    if (res && i < nv) rv[j] = res[i];
+    if (i < nv) hv[j] = x[i];
   }
-  float v[VPT][kVec];
-  float ss = 0.f, m = 0.f;
+  if (a.res) {
+    const uint4* res = reinterpret_cast<const uint4*>(static_cast<const T*>(a.res) + row * a.ldr);
+    uint4* hs = reinterpret_cast<uint4*>(static_cast<T*>(a.h) + row * a.ldh);
+    uint4 rv[VPT];
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      const int i = j * blockDim.x + threadIdx.x;
+      if (i < nv) rv[j] = res[i];
+    }
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      const int i = j * blockDim.x + threadIdx.x;
+      if (i < nv) hs[i] = hv[j] = I::add(hv[j], rv[j]);
+    }
+  }
+  float2 s2 = make_float2(0.f, 0.f);
+  float m = 0.f;
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
     const int i = j * blockDim.x + threadIdx.x;
     if (i >= nv) continue;
-    if (res) {
+    Gain<DT, GF32> g;
+    g.load(a.gain, i);
 #pragma unroll
-      for (int e = 0; e < kVec; ++e) xv[j].v[e] = I::put(I::get(xv[j].v[e]) + I::get(rv[j].v[e]));
-      reinterpret_cast<P*>(static_cast<T*>(a.h) + row * a.ldh)[i] = xv[j];
-    }
-    float g[kVec];
-    if (!a.gain) {
-#pragma unroll
-      for (int e = 0; e < kVec; ++e) g[e] = 1.f;
-    } else if (GF32) {
-#pragma unroll
-      for (int k = 0; k < kVec / 4; ++k) {
-        const G t = reinterpret_cast<const G*>(a.gain)[i * (kVec / 4) + k];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) g[4 * k + e] = t.v[e];
-      }
-    } else {
-      const P t = reinterpret_cast<const P*>(a.gain)[i];
-#pragma unroll
-      for (int e = 0; e < kVec; ++e) g[e] = I::get(t.v[e]);
-    }
-#pragma unroll
-    for (int e = 0; e < kVec; ++e) {
-      const float h = I::get(xv[j].v[e]);
-      ss = fmaf(h, h, ss);
-      v[j][e] = __fmul_rn(h, g[e]);
-      m = nq_max_nan(m, fabsf(v[j][e]));
+    for (int e = 0; e < I::kPairs; ++e) {
+      const float2 h = I::pair(hv[j], e), v = p_mul(h, g.pair(have_g, e));
+      s2 = p_fma(h, h, s2);
+      m = max3_nan(m, fabsf(v.x), fabsf(v.y));
     }
   }
-  float2 sm = block_sum_max(ss, m, sh);
+  float2 sm = block_sum_max(s2.x + s2.y, m, sh);
   float unit = 1.f;
   if (a.norm && sm.x == INFINITY && sm.y < INFINITY) {  // the squares overflow: sum them scaled
     unit = kTiny;
-    ss = 0.f;
+    float ss = 0.f;
 #pragma unroll
     for (int j = 0; j < VPT; ++j)
       if (j * blockDim.x + threadIdx.x < nv)
 #pragma unroll
-        for (int e = 0; e < kVec; ++e) {
-          const float h = I::get(xv[j].v[e]) * kTiny;
-          ss = fmaf(h, h, ss);
+        for (int e = 0; e < I::kPairs; ++e) {
+          const float2 h = p_mul(I::pair(hv[j], e), make_float2(kTiny, kTiny));
+          ss = fmaf(h.x, h.x, fmaf(h.y, h.y, ss));
         }
     sm.x = block_sum_max(ss, 0.f, sh).x;
   }
   const float2 sf = row_scale(a, sm.x, sm.y, unit);
   if (threadIdx.x == 0) a.scale[row] = sf.x;
+  const uint32_t keep = isnan(sf.x) ? 0u : ~0u;
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
     const int i = j * blockDim.x + threadIdx.x;
     if (i >= nv) continue;
-    Q o;
+    Gain<DT, GF32> g;
+    g.load(a.gain, i);
+    uint32_t o[I::kPairs / 2];
 #pragma unroll
-    for (int e = 0; e < kVec; ++e) o.v[e] = isnan(sf.x) ? (int8_t)0 : to_q8(v[j][e], sf.y);
-    reinterpret_cast<Q*>(a.q + row * a.ldq)[i] = o;
+    for (int e = 0; e < I::kPairs; e += 2)
+      o[e / 2] = keep & low_bytes(to_grid(p_mul(I::pair(hv[j], e), g.pair(have_g, e)), sf.y),
+                                  to_grid(p_mul(I::pair(hv[j], e + 1), g.pair(have_g, e + 1)), sf.y));
+    if (I::kPairs == 4) reinterpret_cast<uint2*>(a.q + row * a.ldq)[i] = make_uint2(o[0], o[I::kPairs / 2 - 1]);
+    else reinterpret_cast<uint32_t*>(a.q + row * a.ldq)[i] = o[0];
   }
 }
 
@@ -235,7 +290,7 @@ __global__ void __launch_bounds__(512) rmsnorm_q8_any(NqArgs a) {
 template <int DT, bool GF32>
 static cudaError_t launch_nq(const NormQ8Call& c, const NqArgs& a) {
   using T = typename Io<DT>::T;
-  constexpr int kVec = Io<DT>::kVec;
+  constexpr int kVec = 2 * Io<DT>::kPairs;
   auto ok = [](const void* p, long long ld, size_t es, size_t al) {
     return (uintptr_t)p % al == 0 && (ld * (long long)es) % (long long)al == 0;
   };
