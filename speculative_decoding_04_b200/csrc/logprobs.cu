@@ -541,10 +541,11 @@ struct LbArgs {
   const int32_t* top_idx;
   const float* g_top;
   int V, top, chunks;
-  float inv_T;
+  float inv_T, c;  // 1 / T, log2(e) / T
   int vec;  // every row of logits and grad starts at the same offset within 16 bytes
 };
 
+// Rounding to the logits' type, one value or a 16-byte vector of pairs.
 template <int DT>
 __device__ __forceinline__ typename Elem<DT>::T to_elem(float x);
 template <>
@@ -553,14 +554,33 @@ template <>
 __device__ __forceinline__ __nv_bfloat16 to_elem<DSPARK_BF16>(float x) { return __float2bfloat16_rn(x); }
 template <>
 __device__ __forceinline__ __half to_elem<DSPARK_F16>(float x) { return __float2half_rn(x); }
-
-// A row's coefficients: dl = (indicators) / T + p (k1 log p + k0)
-struct LbRow {
-  float m, logS, inv_T, k1, k0;
-  __device__ __forceinline__ float dense(float x) const {
-    const float lp = fmaxf(fmaf(x - m, inv_T, -logS), -1e4f);  // exp(-1e4) is 0; keeps 0 * inf out
-    return ex2(lp * kLog2e) * fmaf(lp, k1, k0);
+template <int DT>
+__device__ __forceinline__ void put_pair(uint4& o, int i, float2 v) {
+  if (DT == DSPARK_F32) {
+    (i == 0 ? o.x : o.z) = __float_as_uint(v.x);
+    (i == 0 ? o.y : o.w) = __float_as_uint(v.y);
+    return;
   }
+  uint32_t w;
+  if (DT == DSPARK_BF16) {
+    const __nv_bfloat162 t = __floats2bfloat162_rn(v.x, v.y);
+    w = *reinterpret_cast<const uint32_t*>(&t);
+  } else {
+    const __half2 t = __floats2half2_rn(v.x, v.y);
+    w = *reinterpret_cast<const uint32_t*>(&t);
+  }
+  (i == 0 ? o.x : i == 1 ? o.y : i == 2 ? o.z : o.w) = w;
+}
+
+// A row's coefficients: dl = (indicators) / T + p (k1 log2 p + k0), log2 p = (l - m) c - s
+struct LbRow {
+  float m, s, c, k1, k0;
+  __device__ __forceinline__ float2 dense(float2 x) const {
+    float2 lp = p_fma(p_add(x, make_float2(-m, -m)), make_float2(c, c), make_float2(-s, -s));
+    lp = make_float2(fmaxf(lp.x, -1e4f), fmaxf(lp.y, -1e4f));  // 2^-1e4 is 0; keeps 0 * inf out
+    return p_mul(make_float2(ex2(lp.x), ex2(lp.y)), p_fma(lp, make_float2(k1, k1), make_float2(k0, k0)));
+  }
+  __device__ __forceinline__ float dense(float x) const { return dense(make_float2(x, x)).x; }
 };
 
 template <int DT>
@@ -595,6 +615,12 @@ __global__ void __launch_bounds__(kLbThreads) token_logprobs_bwd_kernel(LbArgs a
     }
     return;
   }
+  const int nv = a.vec ? (hi - body) / E::kVec : 0;
+  const uint4* q = reinterpret_cast<const uint4*>(p + body);
+  uint4 v[kLbVecs];
+#pragma unroll
+  for (int j = 0; j < kLbVecs; ++j)
+    if (j * kLbThreads + tid < nv) v[j] = q[j * kLbThreads + tid];
   const float gl = a.g_logp ? __ldg(a.g_logp + n) : 0.f;
   const float gH = a.g_entropy ? __ldg(a.g_entropy + n) : 0.f;
   float G = gl;
@@ -604,9 +630,9 @@ __global__ void __launch_bounds__(kLbThreads) token_logprobs_bwd_kernel(LbArgs a
     if (__ldg(ti + j) >= 0) G += __ldg(gt + j);
   LbRow r;
   r.m = st.x;
-  r.logS = st.y;
-  r.inv_T = a.inv_T;
-  r.k1 = -a.inv_T * gH;
+  r.s = st.y * kLog2e;
+  r.c = a.c;
+  r.k1 = -a.inv_T * gH * (float)kLn2D;
   r.k0 = -a.inv_T * (gH != 0.f ? fmaf(gH, __ldg(a.entropy + n), G) : G);
   if (!(st.x < INFINITY)) r.k0 = __int_as_float(0x7FC00000);  // a row with NaN or +inf: its gradient is NaN
 
@@ -633,24 +659,14 @@ __global__ void __launch_bounds__(kLbThreads) token_logprobs_bwd_kernel(LbArgs a
 
   if (a.vec) {
     for (int i = lo + tid; i < body; i += kLbThreads) g[i] = to_elem<DT>(r.dense(E::get(p[i])));
-    const int nv = (hi - body) / E::kVec;
-    const uint4* q = reinterpret_cast<const uint4*>(p + body);
     uint4* o = reinterpret_cast<uint4*>(g + body);
-    uint4 v[kLbVecs];
-#pragma unroll
-    for (int j = 0; j < kLbVecs; ++j)
-      if (j * kLbThreads + tid < nv) v[j] = q[j * kLbThreads + tid];
 #pragma unroll
     for (int j = 0; j < kLbVecs; ++j)
       if (j * kLbThreads + tid < nv) {
-        T e[E::kVec];
+        uint4 e;
 #pragma unroll
-        for (int i = 0; i < E::kVec / 2; ++i) {
-          const float2 x = E::pair(v[j], i);
-          e[2 * i] = to_elem<DT>(r.dense(x.x));
-          e[2 * i + 1] = to_elem<DT>(r.dense(x.y));
-        }
-        o[j * kLbThreads + tid] = *reinterpret_cast<const uint4*>(e);
+        for (int i = 0; i < E::kVec / 2; ++i) put_pair<DT>(e, i, r.dense(E::pair(v[j], i)));
+        o[j * kLbThreads + tid] = e;
       }
     for (int i = body + nv * E::kVec + tid; i < hi; i += kLbThreads) g[i] = to_elem<DT>(r.dense(E::get(p[i])));
   } else {
@@ -732,7 +748,7 @@ static dspark_status launch_lb(const LogprobsBwdCall& c) {
   const bool vec = ((uintptr_t)c.logits - (uintptr_t)c.grad) % 16 == 0 &&
                    (c.N == 1 || ((c.ld - c.ldg) * (long long)sizeof(T)) % 16 == 0);
   LbArgs a{c.logits, c.grad, c.ld, c.ldg, c.tokens, reinterpret_cast<const float2*>(c.stats), c.entropy, c.g_logp,
-           c.g_entropy, c.top_idx, c.g_top, c.V, c.top, chunks, 1.f / c.T, vec ? 1 : 0};
+           c.g_entropy, c.top_idx, c.g_top, c.V, c.top, chunks, 1.f / c.T, (float)(1.0 / (kLn2D * (double)c.T)), vec ? 1 : 0};
   token_logprobs_bwd_kernel<DT><<<(unsigned)grid, kLbThreads, 0, c.stream>>>(a);
   const cudaError_t rc = cudaGetLastError();
   if (rc != cudaSuccess) {
