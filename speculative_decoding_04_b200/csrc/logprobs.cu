@@ -13,8 +13,10 @@
 // grows.  The sums are fp32 per lane (some 300 terms), joined pairwise over lanes, warps and CTAs; the
 // logarithm and what follows are fp64.
 // The loop costs about 6 instructions a value (packed fp32 pairs; one ex2), which at 16 bits a value is
-// near what the SM can issue while HBM streams: 1088 x 151936 fp32 takes 119 us (5.5 TB/s), 2048 x 262144
-// bf16 192 us.  CTAs of 8 warps, four to an SM, hide each other's row ends better than two of 16 (131
+// near what the SM can issue while HBM streams: 1088 x 151936 fp32 takes 109 us among other calls (6.1
+// TB/s) and 118 after a flush of L2, 2048 x 262144 bf16 188 us.  One row of 151936 with 20 alternatives
+// takes 16 us: a cluster of 16 CTAs, two cluster barriers, the choice of tiles and the candidates between
+// them.  (After a flush of L2:) CTAs of 8 warps, four to an SM, hide each other's row ends better than two of 16 (131
 // against 141 us); a ring filled by 16-byte asynchronous copies measured 139 us (its shared-memory
 // traffic competes with the exponentials), two or three tiles ahead 133 and 143 (fewer warps fit), and
 // rows' values clamped one by one against -inf 204 us in bf16 (hence the two forms of the loop).
@@ -526,8 +528,10 @@ __global__ void __launch_bounds__(W * 32, 32 / W) token_logprobs_kernel(LpArgs a
 
 // ============================================================================ backward
 
-constexpr int kLbThreads = 256;
-constexpr int kLbVecs = 4;
+// 16 KB of a row per CTA, eight vectors a thread in flight.  2048 x 151936 bf16 takes 182 us (6.5 TB/s);
+// 256 threads with 2, 4, 8 or 16 vectors 237, 205, 192 and 211, 128 with 16 186.
+constexpr int kLbThreads = 128;
+constexpr int kLbVecs = 8;
 
 struct LbArgs {
   const void* logits;
