@@ -108,11 +108,12 @@ const char* dspark_last_error(void);
  *                     clusters with double-buffered rows; 0 one cluster per row
  *   "sm_count"        0 query the device, else the SM count used to size persistent grids
  *   "debug_wait_limit", "debug_unreachable_barrier"  test-only: the first shortens the bounded
- *                     device waits (draft: polls per wait; streaming verify: nanoseconds; 0: the
- *                     defaults of about a second and 2 s); the second makes one wait unsatisfiable
+ *                     device waits (draft and 8-bit product: polls per wait; streaming verify:
+ *                     nanoseconds; 0: the defaults of about a second and 2 s); the second makes one wait unsatisfiable
  *                     (1: the fused draft's first grid barrier, 2: the streaming verify's cluster
- *                     exchange), so that a test can check that the kernel returns with
+ *                     exchange, 3: the 8-bit product's accumulators), so that a test can check that the kernel returns with
  *                     DSPARK_ETIMEOUT in the workspace status and DEVICE_TIMEOUT in the flags
+ *                     (the 8-bit product has no workspace: flags, and NaN in the outputs)
  * The environment variables DSPARK_DRAFT_TC_MIN_B, DSPARK_DRAFT_PATH, DSPARK_DRAFT_PDL,
  * DSPARK_DRAFT_FUSED, DSPARK_VERIFY_CLUSTER, DSPARK_VERIFY_PERSISTENT, DSPARK_VERIFY_IMPL,
  * DSPARK_VERIFY_GROUPS and DSPARK_VERIFY_STREAM_CLUSTER set the initial values of the keys of the
@@ -449,8 +450,8 @@ int dspark_token_logprobs(const void* logits, int dtype, int64_t ld, int64_t n_r
  *     grad[n,v] = ( g_logp[n] [v == tok] + sum_j g_top[n,j] [v == top_idx[n,j]]
  *                   - p_v ( G + g_entropy[n] (log p_v + entropy[n]) ) ) / T,
  *     G = g_logp[n] + sum_j g_top[n,j]
- * formed in fp32 and rounded once to dtype.  Entry n is row n of the logits.  Alternatives with index
- * -1 take no part; the same index may occur several times.  Rows without a token (index outside
+ * formed in fp32 and rounded once to dtype.  Entry n is row n of the logits.  Alternatives with an index
+ * outside [0, V), -1 among them, take no part; the same index may occur several times.  Rows without a token (index outside
  * [0, V)) and rows in which everything is masked have gradient 0; rows with NaN or +Inf have NaN.
  * stats     [N, 2] fp32 of the forward call (8-byte aligned); entropy [N] (required with g_entropy).
  * g_logp    [N] fp32 or NULL (0).  g_entropy [N] fp32 or NULL (0).
@@ -485,7 +486,7 @@ int dspark_token_logprobs_backward(const void* logits, int dtype, int64_t ld, co
  *           or the residual itself (same address and stride).
  * q         [M, d] int8, rows ldq bytes apart (a multiple of 16 for dspark_matmul_q8).
  * scale     [M] fp32.
- * M = 0 does nothing.  No workspace.
+ * q and scale overlap no input.  M = 0 does nothing.  No workspace.
  * -------------------------------------------------------------------------- */
 int dspark_rmsnorm_q8(const void* x, int dtype, int64_t ldx, const void* residual, int64_t ldr, const void* gain,
                       int gain_dtype, int M, int d, float eps, void* h_out, int64_t ldh, int8_t* q, int64_t ldq,
@@ -515,7 +516,7 @@ int dspark_quantize_q8(const void* x, int dtype, int64_t ldx, int M, int d, int8
  * out      [M, N] of out_dtype (DSPARK_F32, DSPARK_BF16 or DSPARK_F16), rows ldo elements apart.
  * flags    [M] uint32 or NULL: DEVICE_TIMEOUT where a bounded device wait gave up; the outputs it
  *          could not compute are then NaN.
- * Limits: 1 <= K <= 131071.  M = 0 does nothing.  No workspace.
+ * Limits: 1 <= K <= 131071.  out overlaps no input.  M = 0 does nothing.  No workspace.
  * -------------------------------------------------------------------------- */
 int dspark_matmul_q8(const int8_t* q, int64_t ldq, const float* q_scale, const int8_t* w, int64_t ldw,
                      const float* w_scale, int M, int N, int K, void* out, int out_dtype, int64_t ldo, uint32_t* flags,

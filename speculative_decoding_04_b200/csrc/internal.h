@@ -27,8 +27,8 @@ struct Options {
   int sm_count = 0;              // 0: query the device
   // test-only: make the bounded device waits give up sooner and one of them unsatisfiable, so that
   // a test can check that the kernels return with a timeout status (never on in normal use)
-  long debug_wait_limit = 0;      // draft: polls per wait; streaming verify: nanoseconds (0: defaults)
-  int debug_unreachable_barrier = 0;  // 1: the draft's first grid barrier; 2: the streaming verify's exchange
+  long debug_wait_limit = 0;      // draft, 8-bit product: polls per wait; streaming verify: nanoseconds (0: defaults)
+  int debug_unreachable_barrier = 0;  // 1: the draft's first grid barrier; 2: the streaming verify's exchange; 3: the 8-bit product's accumulators
 };
 // A copy of the process-wide options, taken under their lock (dspark_set_option may run on
 // another thread).

@@ -631,7 +631,7 @@ __global__ void __launch_bounds__(kLbThreads) token_logprobs_bwd_kernel(LbArgs a
   const int32_t* ti = a.top ? a.top_idx + n * a.top : nullptr;
   const float* gt = a.top ? a.g_top + n * a.top : nullptr;
   for (int j = 0; j < a.top; ++j)
-    if (__ldg(ti + j) >= 0) G += __ldg(gt + j);
+    if ((unsigned)__ldg(ti + j) < (unsigned)a.V) G += __ldg(gt + j);
   LbRow r;
   r.m = st.x;
   r.s = st.y * kLog2e;

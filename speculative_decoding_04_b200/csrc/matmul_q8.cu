@@ -8,7 +8,7 @@
 //   warp 0      TMA producer, a ring of stages [BV x 128 B of weights | BN x 128 B of tokens]
 //   warp 1      MMA issuer: per stage 4 steps of K = 32, for one or two blocks of 128 weight rows
 //   warp 2      TMEM allocation
-//   warps 4-11  epilogue: TMEM -> registers, the two scales, stores
+//   warps 4-19  epilogue: TMEM -> registers, the two scales, stores
 // Persistent: one CTA per SM takes tiles in turn, the token tiles of one weight tile next to each
 // other, so that a weight tile comes from HBM once.
 //
@@ -29,8 +29,8 @@ namespace dspark {
 
 namespace {
 
-constexpr int kMqThreads = 384;
-constexpr int kMqEpiWarps = 8;
+constexpr int kMqThreads = 640;
+constexpr int kMqEpiWarps = 16;
 constexpr int kMqKB = 128;    // bytes (= values) of a block of K: one swizzled row
 constexpr int kMqBlocks = 2;  // blocks of K per stage
 constexpr int kMqMaxStages = 8;
@@ -51,6 +51,8 @@ struct MqArgs {
   uint32_t x_off, stage_bytes, bars;    // tokens within a stage; a stage; barriers after the stages
   uint32_t out_off;                     // (CTA pairs) staging of the output
   int out_tma;                          // (CTA pairs) the output takes TMA stores
+  uint32_t spin_limit;                  // polls before a bounded wait gives up
+  int barrier_extra;                    // test-only: arrivals the accumulators' barriers expect beyond the commit
 };
 
 // Tensor maps of the weights and the tokens: [rows, K] with boxes of 128 bytes of K by the tile's rows,
@@ -77,13 +79,14 @@ struct MqRing {
 
 struct MqSync {
   volatile int* abort;
+  uint32_t limit;
 };
 
 // Bounded wait shared by all roles; after any timeout every later wait that has to wait returns at once.
 __device__ __forceinline__ bool mq_wait(const MqSync& s, uint64_t* bar, uint32_t parity) {
   if (mbar_try_wait(bar, parity)) return true;
   if (*s.abort) return false;
-  for (uint32_t i = 0; i < kSpinLimit; ++i) {
+  for (uint32_t i = 0; i < s.limit; ++i) {
     if (mbar_try_wait(bar, parity)) return true;
     if ((i & 1023u) == 1023u && *s.abort) return false;
   }
@@ -132,7 +135,7 @@ __global__ void __launch_bounds__(kMqThreads, 1)
   uint64_t* drain = t_empty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* s_abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  const MqSync sy{s_abort};
+  const MqSync sy{s_abort, a.spin_limit};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int nkb = (a.K + kMqKB - 1) / kMqKB;
 
@@ -142,7 +145,7 @@ __global__ void __launch_bounds__(kMqThreads, 1)
       mbar_init(&empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&t_full[i], 1);
+      mbar_init(&t_full[i], 1 + a.barrier_extra);
       mbar_init(&t_empty[i], kMqEpiWarps);
     }
     mbar_init(drain, 1);
@@ -187,10 +190,10 @@ __global__ void __launch_bounds__(kMqThreads, 1)
           }
         }
       }
-      if (*s_abort)  // let the copies already issued land (bounded) before the CTA exits
-        for (int i = max(0, it - a.stages); i < it; ++i)
-          for (uint32_t n = 0; n < kSpinLimit && !mbar_try_wait(&full[i % a.stages], (i / a.stages) & 1); ++n) {
-          }
+      // the copies already issued land (bounded) before the CTA exits, whoever was to wait for them
+      for (int i = max(0, it - a.stages); i < it; ++i)
+        for (uint32_t n = 0; n < kSpinLimit && !mbar_try_wait(&full[i % a.stages], (i / a.stages) & 1); ++n) {
+        }
     }
   } else if (warp == 1) {
     if (lane == 0) {
@@ -226,13 +229,13 @@ __global__ void __launch_bounds__(kMqThreads, 1)
         }
         if (ok) tc_commit(&t_full[buf]);
       }
-      if (*s_abort) {  // tensor memory and the stages stay until the MMAs already issued are done (bounded)
-        tc_commit(drain);
-        mbar_wait(drain, 0);
-      }
+      tc_commit(drain);  // tensor memory and the stages stay until the MMAs already issued are done (bounded)
+      mbar_wait(drain, 0);
     }
   } else if (warp >= 4) {
-    const int q = warp & 3, b = (warp - 4) >> 2;
+    // lane quadrant, block of 128 weight rows, and which of the alternating chunks of 16 tokens: the last
+    // tile's epilogue runs alone (128 x 50000 x 1024: 25 us, 29 with half as many warps)
+    const int q = warp & 3, b = ((warp - 4) >> 2) & 1, h = (warp - 4) >> 3;
     MqRing acc_r{0, 0};
     for (int t = blockIdx.x; t < a.ntiles; t += gridDim.x, acc_r.next(a.nbuf)) {
       const int buf = acc_r.s;
@@ -252,6 +255,7 @@ __global__ void __launch_bounds__(kMqThreads, 1)
         for (int i = 0; i < kMqMaxTokens / 16; ++i) {
           const int c = i * 16;
           if (c >= nm) break;
+          if ((i & 1) != h) continue;
           uint32_t r[16];
           if (ok) {
             tmem_ld_x16(acc + c, r);
@@ -265,7 +269,7 @@ __global__ void __launch_bounds__(kMqThreads, 1)
               store_out<DT>(a.out, o, ok ? (float)(int32_t)r[j] * s * sw : __int_as_float(0x7FC00000));
           }
         }
-        if (!ok && a.flags && q == 0 && b == 0)
+        if (!ok && a.flags && q == 0 && b == 0 && h == 0)
           for (int m = m0 + lane; m < m0 + nm; m += 32) atomicOr(a.flags + m, DSPARK_FLAG_DEVICE_TIMEOUT);
       }
       tc_fence_before();
@@ -348,7 +352,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   uint64_t* drain = t_empty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* s_abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  const MqSync sy{s_abort};
+  const MqSync sy{s_abort, a.spin_limit};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint32_t rank;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
@@ -362,7 +366,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       mbar_init(&empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&t_full[i], 1);
+      mbar_init(&t_full[i], 1 + a.barrier_extra);
       mbar_init(&t_empty[i], 2 * kPairEpiWarps);
     }
     mbar_init(drain, 1);
@@ -412,9 +416,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           }
         }
       }
-      // after a timeout, rank 0 lets the copies of both CTAs land (bounded); rank 1 waits for it at the
-      // last cluster barrier
-      if (*s_abort && rank == 0)
+      // rank 0 lets the copies of both CTAs land (bounded), whoever was to wait for them; rank 1 waits for
+      // it at the last cluster barrier
+      if (rank == 0)
         for (int i = max(0, it - a.stages); i < it; ++i)
           for (uint32_t n = 0; n < kSpinLimit && !mbar_try_wait(&full[i % a.stages], (i / a.stages) & 1); ++n) {
           }
@@ -451,10 +455,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         }
         if (ok) tc_commit_pair(&t_full[buf]);
       }
-      if (*s_abort) {  // tensor memory and the stages stay until the MMAs already issued are done (bounded)
-        tc_commit_pair(drain);
-        mbar_wait(drain, 0);
-      }
+      tc_commit_pair(drain);  // tensor memory and the stages stay until the MMAs already issued are done (bounded)
+      mbar_wait(drain, 0);
     }
   } else if (warp >= 4) {
     // The four warps of a group h hold 128 consecutive outputs of a token on their lanes.  Chunks of 16
@@ -622,6 +624,9 @@ dspark_status launch_matmul_q8(const MatmulQ8Call& c) {
   a.out = c.out;
   a.ldo = c.ldo;
   a.flags = c.flags;
+  const Options opt = options();
+  a.spin_limit = opt.debug_wait_limit > 0 ? (uint32_t)opt.debug_wait_limit : kSpinLimit;
+  a.barrier_extra = opt.debug_unreachable_barrier == 3 ? 1 : 0;
   a.M = c.M;
   a.N = c.N;
   a.K = c.K;
@@ -648,7 +653,7 @@ dspark_status launch_matmul_q8(const MatmulQ8Call& c) {
     a.out_tma = (uintptr_t)c.out % 16 == 0 && c.ldo * es % 16 == 0 && c.ldo * es < (1ll << 40);
     box_v = 128;
     box_m = a.bn / 2;
-    grid = 2 * std::min(sms / 2, a.ntiles);
+    grid = 2 * std::min(std::max(1, sms / 2), a.ntiles);
   } else {
     // weight rows per tile: the largest tile that gives every CTA the same number of tiles
     // (one token, 151936 x 4096: 115 us; at most 128 rows of 2 or 4 blocks of K 123 and 119, 64 of 8 137)

@@ -211,6 +211,28 @@ def test_two_calls_at_once():
     assert all(torch.equal(o, j[4]) for o, j in zip(outs, jobs))
 
 
+@pytest.mark.parametrize("M", [40, 300])   # one CTA a tile, and CTA pairs
+def test_bounded_waits_return(M):
+    """Accumulator barriers that expect one arrival more than will come: the call returns, its outputs
+    are NaN and its flags say so, and the next call is right.  Nothing faults or hangs."""
+    rng = np.random.default_rng(13)
+    q, w = make_q(rng, M, 300), make_q(rng, 4000, 300)
+    qs, ws = torch.rand(M, device="cuda"), torch.rand(4000, device="cuda")
+    flags = torch.zeros(M, dtype=torch.int32, device="cuda")
+    D.set_option("debug_wait_limit", 1 << 12)
+    D.set_option("debug_unreachable_barrier", 3)
+    out = D.matmul_q8(q, qs, w, ws, flags=flags)
+    torch.cuda.synchronize()
+    assert torch.isnan(out).all()
+    assert np.all(host(flags).view(np.uint32) == np.uint32(D.FLAG_DEVICE_TIMEOUT))
+    D.set_option("debug_unreachable_barrier", 0)
+    D.set_option("debug_wait_limit", 0)
+    flags.zero_()
+    out = D.matmul_q8(q, qs, w, ws, flags=flags)
+    check_matmul(q, qs, w, ws, out, "f32")
+    assert not host(flags).any()
+
+
 def test_empty_batches():
     x = torch.zeros((0, 64), device="cuda")
     q, s, h = D.rmsnorm_q8(x, None, 1e-6, residual=x)

@@ -292,9 +292,10 @@ def test_backward_repeated_indices_masks_and_missing_gradients():
     idx[:, 2] = np.maximum(tok, 0)  # the given token among them
     idx[3, 2] = 0
     idx[:, 3] = -1                 # no alternative
+    idx[:, 4] = [V, 2 ** 31 - 1, -7, V + 1, -2 ** 31, V, -1]   # outside the vocabulary: no alternatives either
     gl, gt = rng.normal(size=N).astype(np.float32), rng.normal(size=(N, 6)).astype(np.float32)
     g = D.token_logprobs_backward(t, dev(tok), T, st, ent, dev(gl), None, top_idx=dev(idx), g_top=dev(gt))
-    grad_check(t, tok, T, gl, None, idx, gt, g, "f32")
+    grad_check(t, tok, T, gl, None, np.where((idx >= 0) & (idx < V), idx, -1), gt, g, "f32")
     gh = rng.normal(size=N).astype(np.float32)
     g = D.token_logprobs_backward(t, dev(tok), T, st, ent, None, dev(gh))
     grad_check(t, tok, T, None, gh, None, None, g, "f32")
