@@ -228,6 +228,30 @@ constexpr int kMaxLogprobsV = 1 << 21;  // 4096 tiles of 2 KB (fp32) whose maxim
 constexpr int kMaxLogprobsN = 1 << 26;  // 16 CTAs each
 constexpr size_t kWsHeader = 256;
 
+// Launch with programmatic dependent launch (the kernel waits for its predecessor with
+// griddepcontrol.wait before it touches global memory), in clusters of `cluster` CTAs if above 1.
+template <typename K, typename A>
+inline cudaError_t launch_dependent(K kernel, long long grid, int block, size_t smem, cudaStream_t stream, int cluster,
+                                    const A& args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3((unsigned)block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.numAttrs = 1;
+  if (cluster > 1) {
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = (unsigned)cluster;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cfg.numAttrs = 2;
+  }
+  cfg.attrs = at;
+  return cudaLaunchKernelEx(&cfg, kernel, args);
+}
+
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 // Element strides of the l_d (or U) row of position k and request b: row = k * sk + b * sb.

@@ -239,9 +239,9 @@ struct WarpSums {
 #pragma unroll
       for (int i = 0; i < kPairs; ++i) {
         const float2 x = E::pair(v[j], i);
-        m = max3_nan(m, x.x, x.y);
+        m = CLAMP ? max3_nan(m, x.x, x.y) : max3(m, x.x, x.y);
       }
-    m = warp_max_nan(m);
+    m = CLAMP ? warp_max_nan(m) : redux_max(m);
     out.put(t, m);
     if (CLAMP) bad |= !(m < INFINITY);  // NaN or +inf
     if (m > R) {                        // the same for all lanes
@@ -317,6 +317,8 @@ __global__ void __launch_bounds__(W * 32, 32 / W) token_logprobs_kernel(LpArgs a
   const int C = CLUSTER ? (int)cluster.num_blocks() : 1, rank = CLUSTER ? (int)cluster.block_rank() : 0;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const long long n = blockIdx.x / C;
+  pdl_wait();
+  pdl_trigger();
   const int tok = __ldg(a.tokens + n);
   const long long row = a.rows ? __ldg(a.rows + n) : n;
 
@@ -605,6 +607,8 @@ __global__ void __launch_bounds__(kLbThreads) token_logprobs_bwd_kernel(LbArgs a
   if (lo >= hi) return;
   const int body = ch == 0 ? head : lo;
 
+  pdl_wait();
+  pdl_trigger();
   const int tok = __ldg(a.tokens + n);
   const float2 st = __ldg(a.stats + n);
   if (tok < 0 || tok >= a.V || st.x == -INFINITY) {  // a row without a token or without any unmasked logit
@@ -691,18 +695,7 @@ static cudaError_t launch_lp(const LpArgs& a, int N, int C, int nt, cudaStream_t
   cudaError_t rc = ensure_smem_attr((const void*)kern, smem);
   if (rc == cudaSuccess && C > 8) rc = ensure_nonportable_cluster((const void*)kern);
   if (rc != cudaSuccess) return rc;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((long long)N * C));
-  cfg.blockDim = dim3(W * 32);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = C;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, a);
+  return launch_dependent(kern, (long long)N * C, W * 32, smem, st, C, a);
 }
 
 template <int DT>
@@ -753,8 +746,7 @@ static dspark_status launch_lb(const LogprobsBwdCall& c) {
                    (c.N == 1 || ((c.ld - c.ldg) * (long long)sizeof(T)) % 16 == 0);
   LbArgs a{c.logits, c.grad, c.ld, c.ldg, c.tokens, reinterpret_cast<const float2*>(c.stats), c.entropy, c.g_logp,
            c.g_entropy, c.top_idx, c.g_top, c.V, c.top, chunks, 1.f / c.T, (float)(1.0 / (kLn2D * (double)c.T)), vec ? 1 : 0};
-  token_logprobs_bwd_kernel<DT><<<(unsigned)grid, kLbThreads, 0, c.stream>>>(a);
-  const cudaError_t rc = cudaGetLastError();
+  const cudaError_t rc = launch_dependent(token_logprobs_bwd_kernel<DT>, grid, kLbThreads, 0, c.stream, 1, a);
   if (rc != cudaSuccess) {
     set_error(std::string("token_logprobs_backward launch: ") + cudaGetErrorString(rc));
     return DSPARK_ECUDA;

@@ -64,6 +64,11 @@ struct MqMaps {
   CUtensorMap out;  // [M, N] of the output's type in boxes of kOutTokens x 128 (CTA pairs, out_tma)
 };
 
+struct MqParams {
+  MqMaps tm;
+  MqArgs a;
+};
+
 // A position in the ring of stages, advanced without divisions: the loops that issue copies and MMAs
 // have a few hundred cycles a stage.
 struct MqRing {
@@ -125,7 +130,9 @@ __device__ __forceinline__ void store_out(void* out, long long i, float v) {
 
 template <int DT>
 __global__ void __launch_bounds__(kMqThreads, 1)
-    matmul_q8_kernel(const __grid_constant__ MqMaps tm, MqArgs a) {
+    matmul_q8_kernel(const __grid_constant__ MqParams p) {
+  const MqMaps& tm = p.tm;
+  const MqArgs& a = p.a;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + a.bars);
@@ -162,6 +169,8 @@ __global__ void __launch_bounds__(kMqThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  pdl_wait();  // barriers and tensor memory are set up while the previous kernel ends
+  pdl_trigger();
 
   if (warp == 0) {
     if (lane == 0) {
@@ -342,7 +351,9 @@ __device__ __forceinline__ void tc_commit_pair(uint64_t* bar) {
 
 template <int DT>
 __global__ void __launch_bounds__(kPairThreads, 1)
-    matmul_q8_pair(const __grid_constant__ MqMaps tm, MqArgs a) {
+    matmul_q8_pair(const __grid_constant__ MqParams p) {
+  const MqMaps& tm = p.tm;
+  const MqArgs& a = p.a;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + a.bars);  // (rank 0) both CTAs' loads of a stage
@@ -386,6 +397,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   cluster_sync_all();  // the peer's barriers are initialised before anything arrives on them
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  pdl_wait();  // barriers and tensor memory are set up while the previous kernel ends
+  pdl_trigger();
 
   if (warp == 0) {
     if (lane == 0) {
@@ -553,13 +566,11 @@ static cudaError_t launch_pair(const MqMaps& tm, const MqArgs& a, int grid, size
 }
 
 template <int DT>
-static cudaError_t launch_mq(const MqMaps& tm, const MqArgs& a, int grid, size_t smem,
-                             cudaStream_t st) {
-  auto kern = matmul_q8_kernel<DT>;
-  cudaError_t rc = ensure_smem_attr((const void*)kern, smem);
+static cudaError_t launch_mq(const MqParams& p, bool pair, int grid, size_t smem, cudaStream_t st) {
+  auto kern = pair ? matmul_q8_pair<DT> : matmul_q8_kernel<DT>;
+  const cudaError_t rc = ensure_smem_attr((const void*)kern, smem);
   if (rc != cudaSuccess) return rc;
-  kern<<<grid, kMqThreads, smem, st>>>(tm, a);
-  return cudaGetLastError();
+  return launch_dependent(kern, grid, pair ? kPairThreads : kMqThreads, smem, st, pair ? 2 : 1, p);
 }
 
 static PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
@@ -618,7 +629,9 @@ static bool out_map(CUtensorMap* m, void* out, int dtype, uint64_t N, uint64_t M
 dspark_status launch_matmul_q8(const MatmulQ8Call& c) {
   if (c.M == 0) return DSPARK_OK;
   const int sms = device_sm_count();
-  MqArgs a{};
+  MqParams p{};
+  MqArgs& a = p.a;
+  MqMaps& tm = p.tm;
   a.q_scale = c.q_scale;
   a.w_scale = c.w_scale;
   a.out = c.out;
@@ -679,7 +692,6 @@ dspark_status launch_matmul_q8(const MatmulQ8Call& c) {
     grid = std::min(sms, a.ntiles);
   }
   const size_t smem = 1024 + a.bars + misc;
-  MqMaps tm{};
   if (pair && a.out_tma && !out_map(&tm.out, c.out, c.out_dtype, c.N, c.M, c.ldo)) {
     set_error("dspark_matmul_q8: cuTensorMapEncodeTiled failed for the output");
     return DSPARK_ECUDA;
@@ -690,15 +702,9 @@ dspark_status launch_matmul_q8(const MatmulQ8Call& c) {
   }
   cudaError_t rc;
   switch (c.out_dtype) {
-    case DSPARK_F32:
-      rc = pair ? launch_pair<DSPARK_F32>(tm, a, grid, smem, c.stream) : launch_mq<DSPARK_F32>(tm, a, grid, smem, c.stream);
-      break;
-    case DSPARK_BF16:
-      rc = pair ? launch_pair<DSPARK_BF16>(tm, a, grid, smem, c.stream) : launch_mq<DSPARK_BF16>(tm, a, grid, smem, c.stream);
-      break;
-    default:
-      rc = pair ? launch_pair<DSPARK_F16>(tm, a, grid, smem, c.stream) : launch_mq<DSPARK_F16>(tm, a, grid, smem, c.stream);
-      break;
+    case DSPARK_F32: rc = launch_mq<DSPARK_F32>(p, pair, grid, smem, c.stream); break;
+    case DSPARK_BF16: rc = launch_mq<DSPARK_BF16>(p, pair, grid, smem, c.stream); break;
+    default: rc = launch_mq<DSPARK_F16>(p, pair, grid, smem, c.stream); break;
   }
   if (rc != cudaSuccess) {
     set_error(std::string("matmul_q8 launch: ") + cudaGetErrorString(rc));

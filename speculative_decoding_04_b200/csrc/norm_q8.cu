@@ -174,6 +174,8 @@ __global__ void __launch_bounds__(VPT == 1 ? 256 : VPT == 2 ? 512 : 1024) rmsnor
   const int nv = a.d / (2 * I::kPairs);
   const bool have_g = a.gain != nullptr;
   const uint4* x = reinterpret_cast<const uint4*>(static_cast<const T*>(a.x) + row * a.ldx);
+  pdl_wait();
+  pdl_trigger();
   uint4 hv[VPT];
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
@@ -255,6 +257,8 @@ __global__ void __launch_bounds__(512) rmsnorm_q8_any(NqArgs a) {
   const T* res = a.res ? static_cast<const T*>(a.res) + row * a.ldr : nullptr;
   T* hs = res ? static_cast<T*>(a.h) + row * a.ldh : nullptr;
   const T* src = res ? hs : x;
+  pdl_wait();
+  pdl_trigger();
   auto gain = [&](int i) {
     return !a.gain ? 1.f : GF32 ? static_cast<const float*>(a.gain)[i] : I::get(static_cast<const T*>(a.gain)[i]);
   };
@@ -300,14 +304,12 @@ static cudaError_t launch_nq(const NormQ8Call& c, const NqArgs& a) {
   if (c.residual) vec = vec && ok(c.residual, c.M > 1 ? c.ldr : 0, sizeof(T), 16) && ok(c.h, c.M > 1 ? c.ldh : 0, sizeof(T), 16);
   if (!vec) {
     const int nt = std::min(512, (c.d + 31) / 32 * 32);
-    rmsnorm_q8_any<DT, GF32><<<(unsigned)c.M, nt, 0, c.stream>>>(a);
-    return cudaGetLastError();
+    return launch_dependent(rmsnorm_q8_any<DT, GF32>, c.M, nt, 0, c.stream, 1, a);
   }
   auto threads = [&](int vpt) { return ((nv + vpt - 1) / vpt + 31) / 32 * 32; };
-  if (threads(1) <= 256) rmsnorm_q8_reg<DT, GF32, 1><<<(unsigned)c.M, threads(1), 0, c.stream>>>(a);
-  else if (threads(2) <= 512) rmsnorm_q8_reg<DT, GF32, 2><<<(unsigned)c.M, threads(2), 0, c.stream>>>(a);
-  else rmsnorm_q8_reg<DT, GF32, 4><<<(unsigned)c.M, threads(4), 0, c.stream>>>(a);
-  return cudaGetLastError();
+  if (threads(1) <= 256) return launch_dependent(rmsnorm_q8_reg<DT, GF32, 1>, c.M, threads(1), 0, c.stream, 1, a);
+  if (threads(2) <= 512) return launch_dependent(rmsnorm_q8_reg<DT, GF32, 2>, c.M, threads(2), 0, c.stream, 1, a);
+  return launch_dependent(rmsnorm_q8_reg<DT, GF32, 4>, c.M, threads(4), 0, c.stream, 1, a);
 }
 
 }  // namespace
