@@ -1,18 +1,22 @@
-"""Build libdspark.so in-tree for sm_100a with nvcc.
+"""Build libdspark.so in-tree for sm_100a with nvcc, and its torch binding with the host compiler.
 
     python -m speculative_decoding_04_b200.build [--verbose]
 
-The library is written to speculative_decoding_04_b200/lib/libdspark.so.
+The library is written to speculative_decoding_04_b200/lib/libdspark.so, the binding (csrc/binding.cpp)
+beside it as the extension module lib/_binding.
 """
 import glob
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 LIB_DIR = os.path.join(HERE, "lib")
 LIB_PATH = os.path.join(LIB_DIR, "libdspark.so")
+BINDING_SRC = os.path.join(HERE, "csrc", "binding.cpp")
+BINDING_PATH = os.path.join(LIB_DIR, "_binding" + sysconfig.get_config_var("EXT_SUFFIX"))
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -41,13 +45,7 @@ def needs_build():
     return any(os.path.getmtime(d) > t for d in deps)
 
 
-def build(verbose=False, force=False, ptxas_verbose=False):
-    if not force and not needs_build():
-        return LIB_PATH
-    os.makedirs(LIB_DIR, exist_ok=True)
-    tmp = LIB_PATH + ".tmp"
-    cmd = [nvcc()] + NVCC_FLAGS + (["-Xptxas", "-v"] if ptxas_verbose else []) + [
-        "-I" + os.path.join(ROOT, "include"), "-shared", "-o", tmp] + sources()
+def run(cmd, what, verbose):
     if verbose:
         print(" ".join(cmd), flush=True)
     r = subprocess.run(cmd, cwd=HERE, capture_output=True, text=True)
@@ -55,9 +53,48 @@ def build(verbose=False, force=False, ptxas_verbose=False):
         sys.stdout.write(r.stdout)
         sys.stderr.write(r.stderr)
     if r.returncode != 0:
-        raise RuntimeError("nvcc failed building libdspark.so")
-    os.replace(tmp, LIB_PATH)
+        raise RuntimeError(f"{cmd[0]} failed building {what}")
+
+
+def needs_binding():
+    if not os.path.exists(BINDING_PATH):
+        return True
+    t = os.path.getmtime(BINDING_PATH)
+    return any(os.path.getmtime(d) > t for d in [BINDING_SRC] + glob.glob(os.path.join(ROOT, "include", "*.h")))
+
+
+def build_binding(verbose=False):
+    import torch
+
+    torch_dir = os.path.dirname(torch.__file__)
+    cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
+    inc = [os.path.join(torch_dir, "include"), os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+           os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
+    tmp = BINDING_PATH + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-DTORCH_EXTENSION_NAME=_binding",
+           "-DTORCH_API_INCLUDE_EXTENSION_H", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+    cmd += ["-isystem" + d for d in inc] + [BINDING_SRC, "-o", tmp, "-L" + LIB_DIR, "-l:libdspark.so",
+                                            "-L" + os.path.join(torch_dir, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu",
+                                            "-ltorch", "-ltorch_python", "-Wl,-rpath,$ORIGIN"]
+    run(cmd, "the torch binding", verbose)
+    os.replace(tmp, BINDING_PATH)
+
+
+def build(verbose=False, force=False, ptxas_verbose=False):
+    if force or needs_build():
+        build_library(verbose, ptxas_verbose)
+    if force or needs_binding():
+        build_binding(verbose)
     return LIB_PATH
+
+
+def build_library(verbose=False, ptxas_verbose=False):
+    os.makedirs(LIB_DIR, exist_ok=True)
+    tmp = LIB_PATH + ".tmp"
+    cmd = [nvcc()] + NVCC_FLAGS + (["-Xptxas", "-v"] if ptxas_verbose else []) + [
+        "-I" + os.path.join(ROOT, "include"), "-shared", "-o", tmp] + sources()
+    run(cmd, "libdspark.so", verbose)
+    os.replace(tmp, LIB_PATH)
 
 
 if __name__ == "__main__":

@@ -1,4 +1,5 @@
-"""Thin ctypes binding of libdspark.so (argument marshalling only).
+"""Thin binding of libdspark.so (argument marshalling only): ctypes, and for the LM-head and
+log-probability calls, which are also made for single tokens, an extension module.
 
 Every function takes CUDA torch tensors, checks dtype / shape / contiguity,
 passes raw device pointers and the current CUDA stream to the C ABI declared
@@ -10,6 +11,7 @@ importing this module raises if the library has not been built.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 import re
 from typing import Optional, Tuple
@@ -17,7 +19,7 @@ from typing import Optional, Tuple
 import numpy as np
 import torch
 
-from .build import LIB_PATH, ROOT
+from .build import BINDING_PATH, LIB_PATH, ROOT
 
 OK, EINVAL, ECUDA, ENOTIMPL, ETIMEOUT = 0, 1, 2, 3, 4
 F32, BF16, F16 = 0, 1, 2
@@ -50,7 +52,6 @@ class DsparkError(RuntimeError):
 
 _vp, _i, _f, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
 _i64 = ctypes.c_int64
-_DTYPES = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
 
 
 def _load() -> ctypes.CDLL:
@@ -110,6 +111,19 @@ def _load() -> ctypes.CDLL:
 
 
 lib = _load()
+
+
+def _load_binding():
+    # the extension module of the LM-head and log-probability entry points (csrc/binding.cpp)
+    if not os.path.exists(BINDING_PATH):
+        raise ImportError(f"{BINDING_PATH} is missing: build it with `python -m speculative_decoding_04_b200.build`")
+    spec = importlib.util.spec_from_file_location("_binding", BINDING_PATH)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    return mod
+
+
+_binding = _load_binding()
 
 
 def declared_functions() -> list:
@@ -470,67 +484,6 @@ def prefix_schedule_t2(c: torch.Tensor, sps: torch.Tensor, D_max: int, ring: tor
     return L_out, a_out, theta_out, K_out, flags
 
 
-def _rows2d(t: torch.Tensor, name: str, dtypes=_DTYPES) -> torch.Tensor:
-    """t as [rows, columns] without a copy: columns dense, rows a constant stride apart."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype not in dtypes:
-        raise ValueError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
-    nd = t.dim()
-    if nd >= 2 and t.is_contiguous():
-        return t if nd == 2 else t.view(-1, t.shape[-1])
-    if nd < 2:
-        raise ValueError(f"{name} must have at least 2 dimensions")
-    if nd > 2:
-        try:
-            t = t.view(-1, t.shape[-1])
-        except RuntimeError as e:
-            raise ValueError(f"{name}: the rows of {tuple(t.shape)} are not a constant stride apart") from e
-    if t.shape[1] > 1 and t.stride(1) != 1:
-        raise ValueError(f"{name}: the last dimension must be dense")
-    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
-        raise ValueError(f"{name}: rows must not overlap")
-    return t
-
-
-def _ld(t: torch.Tensor) -> int:
-    """Row stride of a tensor that passed _rows2d (a single row's stride says nothing)."""
-    return t.stride(0) if t.shape[0] > 1 else max(1, t.shape[1])
-
-
-def _arg(t: Optional[torch.Tensor], name: str, dtype, numel: int, dev) -> Optional[ctypes.c_void_p]:
-    """The address of a contiguous argument of `numel` values on `dev` (None stays None)."""
-    if t is None:
-        return None
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device != dev:
-        raise ValueError(f"{name} must be on {dev}, got {t.device}")
-    if t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.numel() != numel or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous with {numel} values, got {tuple(t.shape)}")
-    return t.data_ptr()
-
-
-# The current stream's handle of a device, without building a Stream object for each call (3 us)
-_raw_stream = torch._C._cuda_getCurrentRawStream
-
-
-def _elsewhere(dev, stream) -> bool:
-    """The call is not for the current device and its current stream."""
-    return stream is not None or dev.index != torch.cuda.current_device()
-
-
-def _at(fn, dev, stream, *args, **kw):
-    """fn with `dev` current and `stream` (or dev's current stream) as its current stream, so that what
-    it allocates belongs to the stream that uses it."""
-    with torch.cuda.device(dev), torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(dev)):
-        return fn(*args, **kw)
-
-
 def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, T: float = 1.0, *, top: int = 0, rows=None, logp=None,
                    entropy=None, top_idx=None, top_logp=None, stats=None, flags=None, stream=None):
     """Log probabilities of `tokens` under rows of `logits` at temperature T, with entropy and the
@@ -541,51 +494,10 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, T: float = 1.0, *
     as tokens).  -1 is an entry without a token.  Returns (logp, entropy, top_idx, top_logp, stats):
     logp and entropy shaped as tokens, the alternatives [..., top] (None when top is 0), stats [..., 2]
     for token_logprobs_backward.  flags: int32, one word per entry, zeroed by the caller, or None."""
-    l2 = _rows2d(logits, "logits")
-    dev = l2.device
-    if _elsewhere(dev, stream):
-        return _at(token_logprobs, dev, stream, logits, tokens, T, top=top, rows=rows, logp=logp, entropy=entropy,
-                   top_idx=top_idx, top_logp=top_logp, stats=stats, flags=flags)
-    top = int(top)
-    N, V = tokens.numel(), l2.shape[1]
-    shape = tokens.shape
-    if top <= 0:
-        top_idx = top_logp = None
-    if logp is None and entropy is None and stats is None and top_idx is None and top_logp is None:
-        # the outputs share one allocation
-        flat = len(shape) == 1
-        if top > 0:
-            stats, logp, entropy, top_logp, top_idx = torch.empty(
-                N * (4 + 2 * top), dtype=torch.float32, device=dev).split_with_sizes((2 * N, N, N, N * top, N * top))
-            alt = (N, top) if flat else shape + (top,)
-            top_logp, top_idx = top_logp.view(alt), top_idx.view(torch.int32).view(alt)
-        else:
-            stats, logp, entropy = torch.empty(4 * N, dtype=torch.float32, device=dev).split_with_sizes((2 * N, N, N))
-        if flat:
-            stats = stats.view(N, 2)
-        else:
-            stats, logp, entropy = stats.view(shape + (2,)), logp.view(shape), entropy.view(shape)
-        outs = [t.data_ptr() for t in (logp, entropy, top_idx, top_logp, stats) if t is not None]
-        if top <= 0:
-            outs[2:2] = (None, None)
-    else:
-        def new(t, tail, dtype):
-            return torch.empty(shape + tail, dtype=dtype, device=dev) if t is None else t
-
-        logp, entropy = new(logp, (), torch.float32), new(entropy, (), torch.float32)
-        stats = new(stats, (2,), torch.float32)
-        if top > 0:
-            top_idx, top_logp = new(top_idx, (top,), torch.int32), new(top_logp, (top,), torch.float32)
-        outs = [_arg(logp, "logp", torch.float32, N, dev), _arg(entropy, "entropy", torch.float32, N, dev),
-                _arg(top_idx, "top_idx", torch.int32, N * top, dev),
-                _arg(top_logp, "top_logp", torch.float32, N * top, dev),
-                _arg(stats, "stats", torch.float32, 2 * N, dev)]
-    st = lib.dspark_token_logprobs(
-        l2.data_ptr(), _DTYPES[l2.dtype], _ld(l2), l2.shape[0], _arg(rows, "rows", torch.int64, N, dev),
-        _arg(tokens, "tokens", torch.int32, N, dev), N, V, float(T), top, *outs,
-        _arg(flags, "flags", torch.int32, N, dev), _raw_stream(dev.index))
-    _check("dspark_token_logprobs", st)
-    return logp, entropy, top_idx, top_logp, stats
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return _binding.token_logprobs(logits, tokens, T, top, rows, logp, entropy, top_idx, top_logp, stats, flags)
+    return _binding.token_logprobs(logits, tokens, T, top, rows, logp, entropy, top_idx, top_logp, stats, flags)
 
 
 def token_logprobs_backward(logits: torch.Tensor, tokens: torch.Tensor, T: float, stats: torch.Tensor,
@@ -598,62 +510,11 @@ def token_logprobs_backward(logits: torch.Tensor, tokens: torch.Tensor, T: float
     forward's top_idx): the gradients of its outputs, each or None.  grad: where to write it -- the
     logits' dtype and shape, the logits themselves among them -- or None: a new tensor with the strides
     of the logits' rows."""
-    l2 = _rows2d(logits, "logits")
-    dev = l2.device
-    if _elsewhere(dev, stream):
-        return _at(token_logprobs_backward, dev, stream, logits, tokens, T, stats, entropy, g_logp, g_entropy,
-                   top_idx=top_idx, g_top=g_top, grad=grad)
-    N, V = l2.shape
-    if tokens.numel() != N:
-        raise ValueError(f"tokens must have one value per row, {N}, got {tokens.numel()}")
-    if (top_idx is None) != (g_top is None):
-        raise ValueError("top_idx and g_top come together")
-    if top_idx is not None and N and top_idx.numel() % N:
-        raise ValueError("top_idx must be [..., top]")
-    top = top_idx.numel() // N if top_idx is not None and N else 0
-    if grad is None:
-        out = torch.empty_strided((N, V), (_ld(l2), 1), dtype=l2.dtype, device=dev)
-        grad = out.view(logits.shape) if logits.dim() > 2 else out
-        g2 = out
-    else:
-        g2 = _rows2d(grad, "grad")
-        if grad.device != dev or grad.dtype != l2.dtype or grad.shape != logits.shape:
-            raise ValueError(f"grad must be {l2.dtype} {tuple(logits.shape)} on {dev}")
-    st = lib.dspark_token_logprobs_backward(
-        l2.data_ptr(), _DTYPES[l2.dtype], _ld(l2), _arg(tokens, "tokens", torch.int32, N, dev), N, V, float(T),
-        _arg(stats, "stats", torch.float32, 2 * N, dev), _arg(entropy, "entropy", torch.float32, N, dev),
-        _arg(g_logp, "g_logp", torch.float32, N, dev), _arg(g_entropy, "g_entropy", torch.float32, N, dev), top,
-        _arg(top_idx, "top_idx", torch.int32, N * top, dev), _arg(g_top, "g_top", torch.float32, N * top, dev),
-        g2.data_ptr(), _ld(g2), _raw_stream(dev.index))
-    _check("dspark_token_logprobs_backward", st)
-    return grad
-
-
-def _q8_out(x, d: int, M: int, q, scale, dev):
-    """The int8 rows and scales of x's rows, given or new, with their addresses and the row stride.
-    New rows start on 16 bytes (what matmul_q8 reads)."""
-    lead = x.shape[:-1]
-    if q is None:
-        ldq = (d + 15) // 16 * 16
-        q = torch.empty(lead + (ldq,), dtype=torch.int8, device=dev)
-        qp = q.data_ptr()
-        if ldq != d:
-            q = q[..., :d]
-    else:
-        t = _like(q, "q", x, torch.int8)
-        qp, ldq = t.data_ptr(), _ld(t)
-    if scale is None:
-        scale = torch.empty(lead, dtype=torch.float32, device=dev)
-        return q, qp, ldq, scale, scale.data_ptr()
-    return q, qp, ldq, scale, _arg(scale, "scale", torch.float32, M, dev)
-
-
-def _like(t: torch.Tensor, name: str, ref: torch.Tensor, dtype) -> torch.Tensor:
-    """t as rows, after checking that it has ref's shape and device and the given dtype."""
-    t2 = _rows2d(t, name, (dtype,))
-    if t.shape != ref.shape or t.device != ref.device:
-        raise ValueError(f"{name} must be {tuple(ref.shape)} on {ref.device}, got {tuple(t.shape)} on {t.device}")
-    return t2
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return _binding.token_logprobs_backward(logits, tokens, T, stats, entropy, g_logp, g_entropy, top_idx, g_top,
+                                                    grad)
+    return _binding.token_logprobs_backward(logits, tokens, T, stats, entropy, g_logp, g_entropy, top_idx, g_top, grad)
 
 
 def rmsnorm_q8(x: torch.Tensor, gain: Optional[torch.Tensor], eps: float, *, residual: Optional[torch.Tensor] = None,
@@ -664,46 +525,18 @@ def rmsnorm_q8(x: torch.Tensor, gain: Optional[torch.Tensor], eps: float, *, res
     or None).  Returns (q [..., d] int8 with rows on 16 bytes, scale [...] fp32, h = x + residual in
     x's dtype, or None without a residual): q * scale is the normalised row.  h_out may be x or the
     residual."""
-    x2 = _rows2d(x, "x")
-    dev = x2.device
-    if _elsewhere(dev, stream):
-        return _at(rmsnorm_q8, dev, stream, x, gain, eps, residual=residual, h_out=h_out, q=q, scale=scale)
-    M, d = x2.shape
-    dt = x2.dtype
-    gdt = dt
-    if gain is not None and gain.dtype != gdt:
-        gdt = torch.float32
-    r2 = h2 = None
-    if residual is not None:
-        r2 = _like(residual, "residual", x, dt)
-        if h_out is None:
-            h_out = torch.empty(x.shape, dtype=dt, device=dev)
-            h2 = h_out.data_ptr(), d
-        else:
-            t = _like(h_out, "h_out", x, dt)
-            h2 = t.data_ptr(), _ld(t)
-    else:
-        h_out = None
-    q, qp, ldq, scale, sp = _q8_out(x, d, M, q, scale, dev)
-    st = lib.dspark_rmsnorm_q8(
-        x2.data_ptr(), _DTYPES[dt], _ld(x2), None if r2 is None else r2.data_ptr(), 0 if r2 is None else _ld(r2),
-        _arg(gain, "gain", gdt, d, dev), _DTYPES[gdt], M, d, float(eps), None if h2 is None else h2[0],
-        0 if h2 is None else h2[1], qp, ldq, sp, _raw_stream(dev.index))
-    _check("dspark_rmsnorm_q8", st)
-    return q, scale, h_out
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return _binding.rmsnorm_q8(x, gain, eps, residual, h_out, q, scale)
+    return _binding.rmsnorm_q8(x, gain, eps, residual, h_out, q, scale)
 
 
 def quantize_q8(x: torch.Tensor, *, q=None, scale=None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """The rows of x [..., d] as int8 with one scale per row: (q, scale), x about q * scale."""
-    x2 = _rows2d(x, "x")
-    dev = x2.device
-    if _elsewhere(dev, stream):
-        return _at(quantize_q8, dev, stream, x, q=q, scale=scale)
-    M, d = x2.shape
-    q, qp, ldq, scale, sp = _q8_out(x, d, M, q, scale, dev)
-    st = lib.dspark_quantize_q8(x2.data_ptr(), _DTYPES[x2.dtype], _ld(x2), M, d, qp, ldq, sp, _raw_stream(dev.index))
-    _check("dspark_quantize_q8", st)
-    return q, scale
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return _binding.quantize_q8(x, q, scale)
+    return _binding.quantize_q8(x, q, scale)
 
 
 def matmul_q8(q: torch.Tensor, q_scale: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor, *,
@@ -713,30 +546,7 @@ def matmul_q8(q: torch.Tensor, q_scale: torch.Tensor, w: torch.Tensor, w_scale: 
     q [..., K] and w [N, K] int8 with rows on 16 bytes (as rmsnorm_q8 and quantize_q8 make them), the
     scales fp32 with one value per row.  out: [..., N] in out_dtype (fp32, bf16 or fp16), or None: a new
     tensor.  With q in the order of U or l_t an fp32 result feeds markov_draft or verify."""
-    q2 = _rows2d(q, "q", (torch.int8,))
-    dev = q2.device
-    if _elsewhere(dev, stream):
-        return _at(matmul_q8, dev, stream, q, q_scale, w, w_scale, out_dtype=out_dtype, out=out, flags=flags)
-    w2 = _rows2d(w, "w", (torch.int8,))
-    if w.dim() != 2 or w.device != dev:
-        raise ValueError(f"w must be [N, K] on {dev}")
-    M, K = q2.shape
-    N = w2.shape[0]
-    if w2.shape[1] != K:
-        raise ValueError(f"q has rows of {K}, w of {w2.shape[1]}")
-    if out is None:
-        if out_dtype not in _DTYPES:
-            raise ValueError(f"out_dtype must be fp32, bf16 or fp16, got {out_dtype}")
-        out = torch.empty(q.shape[:-1] + (N,), dtype=out_dtype, device=dev)
-        ldo = N
-    else:
-        ldo = _ld(_rows2d(out, "out"))
-        if out.device != dev or out.shape != q.shape[:-1] + (N,):
-            raise ValueError(f"out must be {tuple(q.shape[:-1]) + (N,)} on {dev}, got {tuple(out.shape)}")
-    ldq, ldw = (t.stride(0) if t.shape[0] > 1 else (K + 15) // 16 * 16 for t in (q2, w2))
-    st = lib.dspark_matmul_q8(
-        q2.data_ptr(), ldq, _arg(q_scale, "q_scale", torch.float32, M, dev), w2.data_ptr(), ldw,
-        _arg(w_scale, "w_scale", torch.float32, N, dev), M, N, K, out.data_ptr(), _DTYPES[out.dtype], ldo,
-        _arg(flags, "flags", torch.int32, M, dev), _raw_stream(dev.index))
-    _check("dspark_matmul_q8", st)
-    return out
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return _binding.matmul_q8(q, q_scale, w, w_scale, out_dtype, out, flags)
+    return _binding.matmul_q8(q, q_scale, w, w_scale, out_dtype, out, flags)
