@@ -709,8 +709,11 @@ static dspark_status launch_lp(const LogprobsCall& c) {
   while (C < kLpMaxCluster && (long long)c.N * 2 * C <= slots && nt / (2 * C) >= 16) C *= 2;
   LpArgs a{c.logits, c.ld, c.rows, c.n_rows, c.tokens, c.V, c.top, 1.0 / (double)c.T, (float)(1.0 / (kLn2D * (double)c.T)),
            c.logp, c.entropy, c.top_idx, c.top_logp, reinterpret_cast<float2*>(c.stats), c.flags};
+  static const int lpw = getenv("LPW") ? atoi(getenv("LPW")) : 8;
   cudaError_t rc = C > 1 ? launch_lp<DT, 16, true>(a, c.N, C, (int)nt, c.stream)
-                         : launch_lp<DT, 8, false>(a, c.N, C, (int)nt, c.stream);
+                 : lpw == 8 ? launch_lp<DT, 8, false>(a, c.N, C, (int)nt, c.stream)
+                 : lpw == 4 ? launch_lp<DT, 4, false>(a, c.N, C, (int)nt, c.stream)
+                         : launch_lp<DT, 2, false>(a, c.N, C, (int)nt, c.stream);
   if (rc != cudaSuccess && C > 8) {  // no clusters of 16 here
     cudaGetLastError();
     rc = launch_lp<DT, 16, true>(a, c.N, 8, (int)nt, c.stream);

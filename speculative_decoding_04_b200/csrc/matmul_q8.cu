@@ -300,8 +300,9 @@ __global__ void __launch_bounds__(kMqThreads, 1)
 // products of the next.  Rank 0 issues the MMAs; both CTAs' loads complete on rank 0's full barriers,
 // and the commits arrive on both CTAs' empty and accumulator barriers.
 
-constexpr int kPairThreads = 384;
-constexpr int kPairEpiWarps = 8;
+constexpr int kPairGroups = 4;  // of four epilogue warps
+constexpr int kPairEpiWarps = 4 * kPairGroups;
+constexpr int kPairThreads = 128 + 32 * kPairEpiWarps;
 constexpr int kPairMaxStages = 8;
 constexpr int kOutTokens = 16;  // tokens of one staged store
 
@@ -473,47 +474,49 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     }
   } else if (warp >= 4) {
     // The four warps of a group h hold 128 consecutive outputs of a token on their lanes.  Chunks of 16
-    // tokens alternate between the two groups; a chunk is scaled, staged in shared memory as [16][128]
-    // and written by one TMA store (which also clips it to the matrix), two chunks in flight per group.
-    // Rows that do not take TMA stores (not on 16 bytes) are written from the registers: 32 outputs of
-    // one token a store (4096 x 129280 x 2048 in bf16: 919 us with those stores, 778 staged).
-    constexpr uint32_t kOutBytes = kOutTokens * 128u * (DT == DSPARK_F32 ? 4u : 2u);
-    const int q = warp & 3, h = (warp - 4) >> 2;
+    // tokens go to the groups in turn; a chunk is scaled and staged in the group's part of shared memory
+    // while the next one's accumulators are read.  Where rows take TMA stores (16-byte rows) it is staged
+    // as [16][128] and written by one, which also clips it to the matrix.  Other rows are staged at the
+    // offset within 16 bytes that they have in memory, so that aligned 16-byte pieces go from one to the
+    // other, and what is left at either end value by value.
+    constexpr uint32_t kEs = DT == DSPARK_F32 ? 4u : 2u;
+    constexpr uint32_t kPitch = 128u * kEs + 16u;  // a row staged at its offset
+    constexpr int kPieces = (int)kPitch / 16;      // 16-byte pieces it can touch
+    constexpr int kEdge = 16 / (int)kEs;           // values in a piece
+    const int q = warp & 3, h = (warp - 4) >> 2, gt = q * 32 + lane;
     const bool issuer = q == 0 && lane == 0;
-    int staged = 0;
+    uint8_t* stage = sm + a.out_off + (uint32_t)h * (kOutTokens * (a.out_tma ? 128u * kEs : kPitch));
     MqRing acc_r{0, 0};
     for (int t = pair; t < a.ntiles; t += npairs, acc_r.next(2)) {
       const int buf = acc_r.s;
-      const int v0 = (t / a.ntok) * 256 + (int)rank * 128, v = v0 + q * 32 + lane, m0 = (t % a.ntok) * a.bn;
-      const bool mine = v < a.N;
-      const float sw = mine ? __ldg(a.w_scale + v) : 0.f;
+      const int v0 = (t / a.ntok) * 256 + (int)rank * 128, v = v0 + gt, m0 = (t % a.ntok) * a.bn;
+      const float sw = v < a.N ? __ldg(a.w_scale + v) : 0.f;
       const int nm = min(a.bn, a.M - m0);
-      float sq = h * kOutTokens + lane < nm && lane < kOutTokens ? __ldg(a.q_scale + m0 + h * kOutTokens + lane) : 0.f;
+      auto scale_of = [&](int c) {  // lanes 0-15: the tokens' scales of the chunk at c
+        return c + lane < nm && lane < kOutTokens ? __ldg(a.q_scale + m0 + c + lane) : 0.f;
+      };
+      float sq = scale_of(h * kOutTokens);
       const bool ok = __all_sync(0xffffffffu, mq_wait(sy, &t_full[buf], acc_r.phase));
       tc_fence_after();
       const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * a.bn);
-      for (int c = h * kOutTokens; c < nm; c += 2 * kOutTokens) {
-        uint32_t r[16];
-        if (ok) {
-          tmem_ld_x16(acc + c, r);
-          tmem_wait_ld();
-        }
-        const float s_cur = sq;
-        const int cn = c + 2 * kOutTokens + lane;
-        sq = cn < nm && lane < kOutTokens ? __ldg(a.q_scale + m0 + cn) : 0.f;
+      uint32_t r[16];
+      if (ok && h * kOutTokens < nm) tmem_ld_x16(acc + h * kOutTokens, r);
+      for (int c = h * kOutTokens; c < nm; c += kPairGroups * kOutTokens) {
+        if (ok) tmem_wait_ld();
         float o[16];
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
-          const float s = __shfl_sync(0xffffffffu, s_cur, j);
+          const float s = __shfl_sync(0xffffffffu, sq, j);
           o[j] = ok ? (float)(int32_t)r[j] * s * sw : __int_as_float(0x7FC00000);
         }
+        const int cn = c + kPairGroups * kOutTokens;
+        if (ok && cn < nm) tmem_ld_x16(acc + cn, r);
+        sq = scale_of(cn);
         if (a.out_tma) {
-          uint8_t* stage = sm + a.out_off + (uint32_t)(h * 2 + (staged & 1)) * kOutBytes;
-          ++staged;
-          if (issuer) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-          named_bar(1 + h, 128);  // the stage's earlier store has read it
+          if (issuer) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+          named_bar(1 + h, 128);  // the earlier store has read the stage
 #pragma unroll
-          for (int j = 0; j < 16; ++j) store_out<DT>(stage, j * 128 + q * 32 + lane, o[j]);
+          for (int j = 0; j < 16; ++j) store_out<DT>(stage, j * 128 + gt, o[j]);
           fence_proxy_async_smem();
           named_bar(1 + h, 128);
           if (issuer && v0 < a.N) {
@@ -522,10 +525,34 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                          : "memory");
           }
           if (issuer) bulk_commit();
-        } else if (mine) {
+        } else {
+          uint8_t* base = static_cast<uint8_t*>(a.out) + ((long long)(m0 + c) * a.ldo + v0) * kEs;
+          const long long step = a.ldo * kEs;
+          named_bar(1 + h, 128);  // the earlier chunk has left the stage
 #pragma unroll
           for (int j = 0; j < 16; ++j)
-            if (c + j < nm) store_out<DT>(a.out, (long long)(m0 + c + j) * a.ldo + v, o[j]);
+            store_out<DT>(stage + j * kPitch + ((uint32_t)reinterpret_cast<uintptr_t>(base + j * step) & 15u), gt, o[j]);
+          named_bar(1 + h, 128);
+          const int rows = min(kOutTokens, nm - c), bytes = min(128, a.N - v0) * (int)kEs;
+          for (int i = gt; i < rows * kPieces; i += 128) {
+            const int row = i / kPieces, at = (i - row * kPieces) * 16;
+            uint8_t* to = base + row * step;
+            const int shift = (int)((uint32_t)reinterpret_cast<uintptr_t>(to) & 15u);
+            if (at >= shift && at + 16 <= shift + bytes)
+              *reinterpret_cast<uint4*>(to + at - shift) = *reinterpret_cast<const uint4*>(stage + row * kPitch + at);
+          }
+          for (int i = gt; i < rows * 2 * kEdge; i += 128) {  // values e of the first and of the last piece
+            const int row = i / (2 * kEdge), e = i % kEdge;
+            uint8_t* to = base + row * step;
+            const int shift = (int)((uint32_t)reinterpret_cast<uintptr_t>(to) & 15u), end = shift + bytes;
+            const bool last = (i / kEdge) & 1;
+            const int piece = last ? (end - 1) & ~15 : 0, b = piece + e * (int)kEs;
+            const bool whole = piece >= shift && piece + 16 <= end;  // then it was written above
+            if (whole || b < shift || b >= end || (last && piece == 0)) continue;
+            const uint8_t* from = stage + row * kPitch + b;
+            if (kEs == 4) *reinterpret_cast<uint32_t*>(to + b - shift) = *reinterpret_cast<const uint32_t*>(from);
+            else *reinterpret_cast<uint16_t*>(to + b - shift) = *reinterpret_cast<const uint16_t*>(from);
+          }
         }
       }
       if (!ok && a.flags && q == 0 && h == 0)
@@ -659,7 +686,7 @@ dspark_status launch_matmul_q8(const MatmulQ8Call& c) {
     a.x_off = kMqBlocks * a.w_bytes;
     a.stage_bytes = kMqBlocks * (a.w_bytes + a.x_bytes);
     const int es = c.out_dtype == DSPARK_F32 ? 4 : 2;
-    const uint32_t staging = 4u * kOutTokens * 128u * es;
+    const uint32_t staging = kPairGroups * kOutTokens * (128u * es + 16u);
     a.stages = (int)std::min<uint32_t>(kPairMaxStages, (kMqSmem - 1024 - misc - staging) / a.stage_bytes);
     a.out_off = a.stages * a.stage_bytes;
     a.bars = a.out_off + staging;

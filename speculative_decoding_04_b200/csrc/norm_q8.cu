@@ -246,7 +246,70 @@ __global__ void __launch_bounds__(VPT == 1 ? 256 : VPT == 2 ? 512 : 1024) rmsnor
   }
 }
 
-// Any length, stride and alignment: the row is read again from h (or x).
+// Any stride and alignment, EPT values a thread one by one, the row in registers.
+template <int DT, bool GF32, int EPT>
+__global__ void __launch_bounds__(1024) rmsnorm_q8_scalar(NqArgs a) {
+  using I = Io<DT>;
+  using T = typename I::T;
+  __shared__ float sh[64];
+  const long long row = blockIdx.x;
+  const T* x = static_cast<const T*>(a.x) + row * a.ldx;
+  pdl_wait();
+  pdl_trigger();
+  T h[EPT];
+#pragma unroll
+  for (int j = 0; j < EPT; ++j) {
+    const int i = j * blockDim.x + threadIdx.x;
+    h[j] = i < a.d ? x[i] : I::put(0.f);
+  }
+  if (a.res) {
+    const T* res = static_cast<const T*>(a.res) + row * a.ldr;
+    T* hs = static_cast<T*>(a.h) + row * a.ldh;
+    T r[EPT];
+#pragma unroll
+    for (int j = 0; j < EPT; ++j) {
+      const int i = j * blockDim.x + threadIdx.x;
+      r[j] = i < a.d ? res[i] : I::put(0.f);
+    }
+#pragma unroll
+    for (int j = 0; j < EPT; ++j) {
+      const int i = j * blockDim.x + threadIdx.x;
+      h[j] = I::put(I::get(h[j]) + I::get(r[j]));
+      if (i < a.d) hs[i] = h[j];
+    }
+  }
+  auto gain = [&](int i) {
+    return !a.gain || i >= a.d ? 1.f : GF32 ? static_cast<const float*>(a.gain)[i] : I::get(static_cast<const T*>(a.gain)[i]);
+  };
+  float ss = 0.f, m = 0.f;
+#pragma unroll
+  for (int j = 0; j < EPT; ++j) {
+    const float f = I::get(h[j]);
+    ss = fmaf(f, f, ss);
+    m = nq_max_nan(m, fabsf(__fmul_rn(f, gain(j * blockDim.x + threadIdx.x))));
+  }
+  float2 sm = block_sum_max(ss, m, sh);
+  float unit = 1.f;
+  if (a.norm && sm.x == INFINITY && sm.y < INFINITY) {  // the squares overflow: sum them scaled
+    unit = kTiny;
+    ss = 0.f;
+#pragma unroll
+    for (int j = 0; j < EPT; ++j) {
+      const float f = I::get(h[j]) * kTiny;
+      ss = fmaf(f, f, ss);
+    }
+    sm.x = block_sum_max(ss, 0.f, sh).x;
+  }
+  const float2 sf = row_scale(a, sm.x, sm.y, unit);
+  if (threadIdx.x == 0) a.scale[row] = sf.x;
+#pragma unroll
+  for (int j = 0; j < EPT; ++j) {
+    const int i = j * blockDim.x + threadIdx.x;
+    if (i < a.d) a.q[row * a.ldq + i] = isnan(sf.x) ? (int8_t)0 : to_q8(__fmul_rn(I::get(h[j]), gain(i)), sf.y);
+  }
+}
+
+// Longer rows: read again from h (or x).
 template <int DT, bool GF32>
 __global__ void __launch_bounds__(512) rmsnorm_q8_any(NqArgs a) {
   using I = Io<DT>;
@@ -303,7 +366,11 @@ static cudaError_t launch_nq(const NormQ8Call& c, const NqArgs& a) {
              (uintptr_t)c.gain % 16 == 0 && nv <= 4 * 1024;
   if (c.residual) vec = vec && ok(c.residual, c.M > 1 ? c.ldr : 0, sizeof(T), 16) && ok(c.h, c.M > 1 ? c.ldh : 0, sizeof(T), 16);
   if (!vec) {
-    const int nt = std::min(512, (c.d + 31) / 32 * 32);
+    // 8 values a thread, then 16 (46 rows of 12271: NQS us; two passes over the row in memory NQA us)
+    auto scalar_threads = [&](int ept) { return ((c.d + ept - 1) / ept + 31) / 32 * 32; };
+    if (scalar_threads(8) <= 1024) return launch_dependent(rmsnorm_q8_scalar<DT, GF32, 8>, c.M, scalar_threads(8), 0, c.stream, 1, a);
+    if (scalar_threads(16) <= 1024) return launch_dependent(rmsnorm_q8_scalar<DT, GF32, 16>, c.M, scalar_threads(16), 0, c.stream, 1, a);
+    const int nt = 512;
     return launch_dependent(rmsnorm_q8_any<DT, GF32>, c.M, nt, 0, c.stream, 1, a);
   }
   auto threads = [&](int vpt) { return ((nv + vpt - 1) / vpt + 31) / 32 * 32; };
