@@ -420,7 +420,7 @@ __global__ void __launch_bounds__(W * 32, 32 / W) token_logprobs_kernel(LpArgs a
     __syncthreads();
 
     // -------------------------------------------------------------- their candidates
-    const int nsel = s_nsel;
+    const int nsel = s_nsel, room = nsel > 0 ? a.top * a.top / nsel : 0;
     const float thr = s_thr;
     uint64_t* cand = CLUSTER ? cluster.map_shared_rank(s_cand, 0) : s_cand;
     int* ncand = CLUSTER ? cluster.map_shared_rank(&s_ncand, 0) : &s_ncand;
@@ -433,19 +433,39 @@ __global__ void __launch_bounds__(W * 32, 32 / W) token_logprobs_kernel(LpArgs a
         return (q & 1) ? f.y : f.x;
       };
       auto index = [&](int q) { return ((q / E::kVec) * 32 + lane) * E::kVec + q % E::kVec; };
-      uint32_t in = 0;  // this lane's values at or above the threshold
+      auto at_least = [&](float t) {  // this lane's unmasked values at or above t, as bits
+        uint32_t in = 0;
 #pragma unroll
-      for (int q = 0; q < kLoads * E::kVec; ++q)
-        if (value(q) >= thr && value(q) > -INFINITY) in |= 1u << q;
-      const int all = __reduce_add_sync(0xffffffffu, __popc(in));
-      if (all <= a.top) {
+        for (int q = 0; q < kLoads * E::kVec; ++q)
+          if (value(q) >= t && value(q) > -INFINITY) in |= 1u << q;
+        return in;
+      };
+      // (nsel tiles share room for top^2 candidates)
+      uint32_t in = at_least(thr);
+      int all = __reduce_add_sync(0xffffffffu, __popc(in));
+      if (all > room) {
+        // too many: `top` lanes hold a value at or above the top-th largest lane maximum
+        float lane_max = -INFINITY, t = -INFINITY;
+#pragma unroll
+        for (int q = 0; q < kLoads * E::kVec; ++q) lane_max = fmaxf(lane_max, value(q));
+        for (int k = 0; k < a.top; ++k) {
+          t = redux_max(lane_max);
+          const unsigned who = __ballot_sync(0xffffffffu, lane_max == t);
+          if (lane == __ffs(who) - 1) lane_max = -INFINITY;
+        }
+        if (t > thr) {
+          in = at_least(t);
+          all = __reduce_add_sync(0xffffffffu, __popc(in));
+        }
+      }
+      if (all <= room) {
         if (in) {
           int at = atomicAdd(ncand, __popc(in));
 #pragma unroll
           for (int q = 0; q < kLoads * E::kVec; ++q)
             if (in >> q & 1) cand[at++] = cand_key(value(q), (uint32_t)(ts + index(q)));
         }
-      } else {  // more than `top`: take the best ones in turn
+      } else {  // many equal values: take the best ones in turn
         for (int round = 0; round < a.top; ++round) {
           float best = -INFINITY;
           int bq = -1;
@@ -709,11 +729,11 @@ static dspark_status launch_lp(const LogprobsCall& c) {
   while (C < kLpMaxCluster && (long long)c.N * 2 * C <= slots && nt / (2 * C) >= 16) C *= 2;
   LpArgs a{c.logits, c.ld, c.rows, c.n_rows, c.tokens, c.V, c.top, 1.0 / (double)c.T, (float)(1.0 / (kLn2D * (double)c.T)),
            c.logp, c.entropy, c.top_idx, c.top_logp, reinterpret_cast<float2*>(c.stats), c.flags};
-  static const int lpw = getenv("LPW") ? atoi(getenv("LPW")) : 8;
-  cudaError_t rc = C > 1 ? launch_lp<DT, 16, true>(a, c.N, C, (int)nt, c.stream)
-                 : lpw == 8 ? launch_lp<DT, 8, false>(a, c.N, C, (int)nt, c.stream)
-                 : lpw == 4 ? launch_lp<DT, 4, false>(a, c.N, C, (int)nt, c.stream)
-                         : launch_lp<DT, 2, false>(a, c.N, C, (int)nt, c.stream);
+  // warps per CTA by the row's tiles, so that a warp has enough of them for the row's end to cost little
+  // (2, 4 and 8 warps: 2000 x 12000 fp32 23.5, 24.9 and 29.8 us; 700 x 50000 fp32 38, 30.5 and 34 us;
+  // 1000 x 100001 bf16 77, 61 and 57 us)
+  auto one = nt <= 32 ? launch_lp<DT, 2, false> : nt <= 128 ? launch_lp<DT, 4, false> : launch_lp<DT, 8, false>;
+  cudaError_t rc = C > 1 ? launch_lp<DT, 16, true>(a, c.N, C, (int)nt, c.stream) : one(a, c.N, 1, (int)nt, c.stream);
   if (rc != cudaSuccess && C > 8) {  // no clusters of 16 here
     cudaGetLastError();
     rc = launch_lp<DT, 16, true>(a, c.N, 8, (int)nt, c.stream);
