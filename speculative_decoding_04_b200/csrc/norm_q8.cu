@@ -11,7 +11,8 @@
 // or not aligned for that are read again from the stored h.  Bound by HBM: 16384 rows of 5120 bf16 with a
 // residual take 92 us (6.4 TB/s).  What it took to get there is few instructions: with one value at a
 // time the same launch shape measured 127 us, three quarters of its issue slots busy.  A persistent grid
-// that loads a row ahead measured 207 us (the registers of two rows leave too few warps).
+// that loads a row ahead measured 207 us (the registers of two rows leave too few warps).  Rows of odd
+// length have a form of their own: 5000 x 4095 bf16 42 us, value by value 67 (5000 x 4096: 24).
 
 #include <cuda_fp16.h>
 
@@ -246,6 +247,188 @@ __global__ void __launch_bounds__(VPT == 1 ? 256 : VPT == 2 ? 512 : 1024) rmsnor
   }
 }
 
+// Gains of the kN values from element i on, i anything: the 16-byte vectors they lie in, shifted (what
+// of them lies past the d gains is not read).
+template <int DT, bool GF32>
+struct GainAt {
+  static constexpr int kN = 2 * Io<DT>::kPairs;           // values
+  static constexpr int kPer = GF32 ? 4 : kN;              // gains in a vector
+  static constexpr int kVecs = kN / kPer + 1;
+  static constexpr int kWords = GF32 ? kN : kN * (int)sizeof(typename Io<DT>::T) / 4;
+  uint32_t w[kWords];
+  __device__ __forceinline__ void load(const void* gain, int i, int d) {
+    if (!gain) return;
+    const uint4* g = static_cast<const uint4*>(gain) + i / kPer;
+    const int off = i % kPer;
+    uint32_t in[kVecs * 4];
+#pragma unroll
+    for (int k = 0; k < kVecs; ++k) {
+      uint4 t = make_uint4(0, 0, 0, 0);
+      if (k < kVecs - 1 || off) {
+        const int end = (i / kPer + k + 1) * kPer;  // past the vector's last gain
+        if (end <= d) t = __ldg(g + k);
+        else t = partial(gain, end - kPer, d);
+      }
+      in[4 * k] = t.x;
+      in[4 * k + 1] = t.y;
+      in[4 * k + 2] = t.z;
+      in[4 * k + 3] = t.w;
+    }
+    // off is the same for all threads of a row: a shift by words, then by half a word
+    constexpr bool kHalves = !GF32 && sizeof(typename Io<DT>::T) == 2;
+    const int words = kHalves ? off >> 1 : off;
+    const int n_in = kWords + (kHalves ? 1 : 0);
+    uint32_t a[kWords + 1];
+#pragma unroll
+    for (int k = 0; k < n_in; ++k) {
+      uint32_t t = in[k];
+#pragma unroll
+      for (int o = 1; o < 4; ++o)
+        if (words == o && k + o < kVecs * 4) t = in[k + o];
+      a[k] = t;
+    }
+#pragma unroll
+    for (int k = 0; k < kWords; ++k) w[k] = kHalves && (off & 1) ? __funnelshift_r(a[k], a[k + 1], 16) : a[k];
+  }
+  // the gains from element i to d - 1, one at a time
+  static __device__ __forceinline__ uint4 partial(const void* gain, int i, int d) {
+    uint32_t w[4] = {0, 0, 0, 0};
+    for (int e = 0; i + e < d; ++e) {
+      if (GF32 || DT == DSPARK_F32) w[e & 3] = static_cast<const uint32_t*>(gain)[i + e];
+      else w[(e >> 1) & 3] |= (uint32_t)static_cast<const uint16_t*>(gain)[i + e] << (16 * (e & 1));
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  __device__ __forceinline__ float2 pair(bool have, int e) const {
+    if (!have) return make_float2(1.f, 1.f);
+    if (GF32 || DT == DSPARK_F32) return make_float2(__uint_as_float(w[2 * e]), __uint_as_float(w[2 * e + 1]));
+    return Io<DT>::pair(make_uint4(w[e], 0, 0, 0), 0);
+  }
+};
+
+// Rows that start anywhere within 16 bytes (odd lengths), x, residual and h alike: the vectors of
+// rmsnorm_q8_reg from the first 16-byte boundary on, the few values before and behind them one to a
+// thread, and q assembled in shared memory, since its rows are aligned where x's are not.
+template <int DT, bool GF32, int VPT>
+__global__ void __launch_bounds__(VPT == 1 ? 256 : VPT == 2 ? 512 : 1024) rmsnorm_q8_shift(NqArgs a) {
+  using I = Io<DT>;
+  using T = typename I::T;
+  constexpr int kVec = 2 * I::kPairs;
+  extern __shared__ __align__(16) uint8_t s_q[];  // value e of the row at byte e - head + 8
+  __shared__ float sh[64];
+  const long long row = blockIdx.x;
+  const bool have_g = a.gain != nullptr;
+  const T* x = static_cast<const T*>(a.x) + row * a.ldx;
+  const T* res = a.res ? static_cast<const T*>(a.res) + row * a.ldr : nullptr;
+  T* hs = a.res ? static_cast<T*>(a.h) + row * a.ldh : nullptr;
+  const int head = min(a.d, (int)(((16u - ((uint32_t)reinterpret_cast<uintptr_t>(x) & 15u)) & 15u) / sizeof(T)));
+  const int nv = (a.d - head) / kVec, tail = a.d - head - nv * kVec;
+  // the value this thread has beside its vectors, or none
+  const int edge = (int)threadIdx.x < head            ? (int)threadIdx.x
+                   : (int)threadIdx.x < head + tail ? nv * kVec + (int)threadIdx.x
+                                                    : -1;
+  pdl_wait();
+  pdl_trigger();
+  uint4 hv[VPT];
+  float he = 0.f, ge = 1.f;
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) {
+    const int i = j * blockDim.x + threadIdx.x;
+    if (i < nv) hv[j] = reinterpret_cast<const uint4*>(x + head)[i];
+  }
+  if (edge >= 0) {
+    he = I::get(x[edge]);
+    if (have_g) ge = GF32 ? static_cast<const float*>(a.gain)[edge] : I::get(static_cast<const T*>(a.gain)[edge]);
+  }
+  if (res) {
+    uint4 rv[VPT];
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      const int i = j * blockDim.x + threadIdx.x;
+      if (i < nv) rv[j] = reinterpret_cast<const uint4*>(res + head)[i];
+    }
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      const int i = j * blockDim.x + threadIdx.x;
+      if (i < nv) reinterpret_cast<uint4*>(hs + head)[i] = hv[j] = I::add(hv[j], rv[j]);
+    }
+    if (edge >= 0) {
+      const T t = I::put(he + I::get(res[edge]));
+      hs[edge] = t;
+      he = I::get(t);
+    }
+  }
+  constexpr bool kKeep = VPT <= 2;  // v stays in registers: the shifted gains cost more than they
+  float2 v[kKeep ? VPT : 1][I::kPairs];
+  float2 s2 = make_float2(0.f, 0.f);
+  float m = 0.f;
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) {
+    const int i = j * blockDim.x + threadIdx.x;
+    if (i >= nv) continue;
+    GainAt<DT, GF32> g;
+    g.load(a.gain, head + i * kVec, a.d);
+#pragma unroll
+    for (int e = 0; e < I::kPairs; ++e) {
+      const float2 h = I::pair(hv[j], e), t = p_mul(h, g.pair(have_g, e));
+      if (kKeep) v[kKeep ? j : 0][e] = t;
+      s2 = p_fma(h, h, s2);
+      m = max3_nan(m, fabsf(t.x), fabsf(t.y));
+    }
+  }
+  s2.x = fmaf(he, he, s2.x);
+  m = nq_max_nan(m, fabsf(__fmul_rn(he, ge)));
+  float2 sm = block_sum_max(s2.x + s2.y, m, sh);
+  float unit = 1.f;
+  if (a.norm && sm.x == INFINITY && sm.y < INFINITY) {  // the squares overflow: sum them scaled
+    unit = kTiny;
+    float ss = he * kTiny * (he * kTiny);
+#pragma unroll
+    for (int j = 0; j < VPT; ++j)
+      if (j * blockDim.x + threadIdx.x < nv)
+#pragma unroll
+        for (int e = 0; e < I::kPairs; ++e) {
+          const float2 h = p_mul(I::pair(hv[j], e), make_float2(kTiny, kTiny));
+          ss = fmaf(h.x, h.x, fmaf(h.y, h.y, ss));
+        }
+    sm.x = block_sum_max(ss, 0.f, sh).x;
+  }
+  const float2 sf = row_scale(a, sm.x, sm.y, unit);
+  if (threadIdx.x == 0) a.scale[row] = sf.x;
+  const uint32_t keep = isnan(sf.x) ? 0u : ~0u;
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) {
+    const int i = j * blockDim.x + threadIdx.x;
+    if (i >= nv) continue;
+    GainAt<DT, GF32> g;
+    if (!kKeep) g.load(a.gain, head + i * kVec, a.d);
+    auto again = [&](int e) { return kKeep ? v[kKeep ? j : 0][e] : p_mul(I::pair(hv[j], e), g.pair(have_g, e)); };
+    uint32_t o[I::kPairs / 2];
+#pragma unroll
+    for (int e = 0; e < I::kPairs; e += 2)
+      o[e / 2] = keep & low_bytes(to_grid(again(e), sf.y), to_grid(again(e + 1), sf.y));
+    if (I::kPairs == 4) *reinterpret_cast<uint2*>(s_q + 8 + i * kVec) = make_uint2(o[0], o[I::kPairs / 2 - 1]);
+    else *reinterpret_cast<uint32_t*>(s_q + 8 + i * kVec) = o[0];
+  }
+  if (edge >= 0) s_q[edge - head + 8] = keep ? (uint8_t)to_q8(__fmul_rn(he, ge), sf.y) : (uint8_t)0;
+  __syncthreads();
+  int8_t* q = a.q + row * a.ldq;
+  for (int c = threadIdx.x * 16; c < a.d; c += blockDim.x * 16) {
+    const int p = c - head + 8;
+    if (c + 16 <= a.d) {
+      const uint32_t* w = reinterpret_cast<const uint32_t*>(s_q + (p & ~3));
+      const int sft = 8 * (p & 3);
+      uint32_t t[5];
+#pragma unroll
+      for (int k = 0; k < 5; ++k) t[k] = w[k];
+      *reinterpret_cast<uint4*>(q + c) = make_uint4(__funnelshift_r(t[0], t[1], sft), __funnelshift_r(t[1], t[2], sft),
+                                                    __funnelshift_r(t[2], t[3], sft), __funnelshift_r(t[3], t[4], sft));
+    } else {
+      for (int k = 0; c + k < a.d; ++k) q[c + k] = (int8_t)s_q[p + k];
+    }
+  }
+}
+
 // Any stride and alignment, EPT values a thread one by one, the row in registers.
 template <int DT, bool GF32, int EPT>
 __global__ void __launch_bounds__(1024) rmsnorm_q8_scalar(NqArgs a) {
@@ -365,15 +548,25 @@ static cudaError_t launch_nq(const NormQ8Call& c, const NqArgs& a) {
   bool vec = c.d % kVec == 0 && ok(c.x, c.M > 1 ? c.ldx : 0, sizeof(T), 16) && ok(c.q, c.M > 1 ? c.ldq : 0, 1, kVec) &&
              (uintptr_t)c.gain % 16 == 0 && nv <= 4 * 1024;
   if (c.residual) vec = vec && ok(c.residual, c.M > 1 ? c.ldr : 0, sizeof(T), 16) && ok(c.h, c.M > 1 ? c.ldh : 0, sizeof(T), 16);
-  if (!vec) {
-    // 8 values a thread, then 16 (46 rows of 12271: NQS us; two passes over the row in memory NQA us)
-    auto scalar_threads = [&](int ept) { return ((c.d + ept - 1) / ept + 31) / 32 * 32; };
-    if (scalar_threads(8) <= 1024) return launch_dependent(rmsnorm_q8_scalar<DT, GF32, 8>, c.M, scalar_threads(8), 0, c.stream, 1, a);
-    if (scalar_threads(16) <= 1024) return launch_dependent(rmsnorm_q8_scalar<DT, GF32, 16>, c.M, scalar_threads(16), 0, c.stream, 1, a);
-    const int nt = 512;
-    return launch_dependent(rmsnorm_q8_any<DT, GF32>, c.M, nt, 0, c.stream, 1, a);
-  }
   auto threads = [&](int vpt) { return ((nv + vpt - 1) / vpt + 31) / 32 * 32; };
+  if (!vec) {
+    // x, residual and h start every row at the same offset within 16 bytes, q and the gains on 16
+    const size_t es = sizeof(T);
+    auto alike = [&](const void* p, long long ld) {
+      return ((uintptr_t)p - (uintptr_t)c.x) % 16 == 0 && (c.M == 1 || (ld - c.ldx) * (long long)es % 16 == 0);
+    };
+    const bool shift = nv >= 16 && nv <= 4 * 1024 && ok(c.q, c.M > 1 ? c.ldq : 0, 1, 16) && (uintptr_t)c.gain % 16 == 0 &&
+                       (!c.residual || (alike(c.residual, c.ldr) && alike(c.h, c.ldh)));
+    if (shift) {
+      const size_t smem = (size_t)c.d + 64;
+      if (threads(1) <= 256) return launch_dependent(rmsnorm_q8_shift<DT, GF32, 1>, c.M, threads(1), smem, c.stream, 1, a);
+      if (threads(2) <= 512) return launch_dependent(rmsnorm_q8_shift<DT, GF32, 2>, c.M, threads(2), smem, c.stream, 1, a);
+      return launch_dependent(rmsnorm_q8_shift<DT, GF32, 4>, c.M, threads(4), smem, c.stream, 1, a);
+    }
+    const int nt8 = ((c.d + 7) / 8 + 31) / 32 * 32;
+    if (nt8 <= 1024) return launch_dependent(rmsnorm_q8_scalar<DT, GF32, 8>, c.M, nt8, 0, c.stream, 1, a);
+    return launch_dependent(rmsnorm_q8_any<DT, GF32>, c.M, 512, 0, c.stream, 1, a);
+  }
   if (threads(1) <= 256) return launch_dependent(rmsnorm_q8_reg<DT, GF32, 1>, c.M, threads(1), 0, c.stream, 1, a);
   if (threads(2) <= 512) return launch_dependent(rmsnorm_q8_reg<DT, GF32, 2>, c.M, threads(2), 0, c.stream, 1, a);
   return launch_dependent(rmsnorm_q8_reg<DT, GF32, 4>, c.M, threads(4), 0, c.stream, 1, a);
