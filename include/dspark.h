@@ -516,7 +516,7 @@ int dspark_quantize_q8(const void* x, int dtype, int64_t ldx, int M, int d, int8
  * out      [M, N] of out_dtype (DSPARK_F32, DSPARK_BF16 or DSPARK_F16), rows ldo elements apart.
  * flags    [M] uint32 or NULL: DEVICE_TIMEOUT where a bounded device wait gave up; the outputs it
  *          could not compute are then NaN.
- * Limits: 1 <= K <= 131071.  out overlaps no input.  M = 0 does nothing.  No workspace.
+ * Limits: 1 <= K <= 131071; M, N <= 2^30 and M * N below about 2^39.  out overlaps no input.  M = 0 does nothing.  No workspace.
  * -------------------------------------------------------------------------- */
 int dspark_matmul_q8(const int8_t* q, int64_t ldq, const float* q_scale, const int8_t* w, int64_t ldw,
                      const float* w_scale, int M, int N, int K, void* out, int out_dtype, int64_t ldo, uint32_t* flags,

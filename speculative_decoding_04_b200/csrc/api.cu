@@ -420,7 +420,8 @@ int dspark_matmul_q8(const int8_t* q, int64_t ldq, const float* q_scale, const i
   if (!q || !q_scale || !w || !w_scale || !out) return einval("dspark_matmul_q8: null pointer");
   if ((uintptr_t)q % 16 || (uintptr_t)w % 16) return einval("dspark_matmul_q8: q and w must be 16-byte aligned");
   if ((uintptr_t)out % es) return einval("dspark_matmul_q8: out must be aligned to its type");
-  if ((long long)(M / 16 + 1) * (N / 16 + 1) >= (1ll << 31)) return einval("dspark_matmul_q8: product too large");
+  if (M > (1 << 30) || N > (1 << 30) || (long long)(M / 16 + 1) * (N / 16 + 1) >= (1ll << 31))
+    return einval("dspark_matmul_q8: product too large");
   MatmulQ8Call c{q, ldq, q_scale, w, ldw, w_scale, M, N, K, out, out_dtype, ldo, flags, (cudaStream_t)stream};
   return launch_matmul_q8(c);
 }

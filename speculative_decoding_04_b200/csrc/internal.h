@@ -228,8 +228,9 @@ constexpr int kMaxLogprobsV = 1 << 21;  // 4096 tiles of 2 KB (fp32) whose maxim
 constexpr int kMaxLogprobsN = 1 << 26;  // 16 CTAs each
 constexpr size_t kWsHeader = 256;
 
-// Launch with programmatic dependent launch (the kernel waits for its predecessor with
-// griddepcontrol.wait before it touches global memory), in clusters of `cluster` CTAs if above 1.
+// Launch with programmatic dependent launch, in clusters of `cluster` CTAs if above 1.  The kernel waits
+// for its predecessor with griddepcontrol.wait before it touches global memory, and reads nothing that a
+// predecessor may have written by the read-only path (__ldg), which may be moved above that wait.
 template <typename K, typename A>
 inline cudaError_t launch_dependent(K kernel, long long grid, int block, size_t smem, cudaStream_t stream, int cluster,
                                     const A& args) {

@@ -147,7 +147,7 @@ struct RowTiles {
     if (len == kTile) {
       const uint4* q = reinterpret_cast<const uint4*>(p + s) + lane;
 #pragma unroll
-      for (int j = 0; j < kLoads; ++j) v[j] = __ldg(q + j * 32);
+      for (int j = 0; j < kLoads; ++j) v[j] = q[j * 32];
     } else {
       load_edge(s, len, lane, v);
     }
@@ -319,8 +319,8 @@ __global__ void __launch_bounds__(W * 32, 32 / W) token_logprobs_kernel(LpArgs a
   const long long n = blockIdx.x / C;
   pdl_wait();
   pdl_trigger();
-  const int tok = __ldg(a.tokens + n);
-  const long long row = a.rows ? __ldg(a.rows + n) : n;
+  const int tok = a.tokens[n];
+  const long long row = a.rows ? a.rows[n] : n;
 
   if (tok == -1 || row < 0 || row >= a.n_rows) {  // the whole cluster leaves
     if (rank == 0) {
@@ -344,6 +344,7 @@ __global__ void __launch_bounds__(W * 32, 32 / W) token_logprobs_kernel(LpArgs a
   const int nt = tiles.n;
   if (tid == 0) s_ncand = 0;
   // the peers have started before anything is written to them (waited for below)
+  __syncwarp();
   if (CLUSTER) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   const bool in_range = (unsigned)tok < (unsigned)a.V;
   float x_tok = 0.f;
@@ -353,6 +354,7 @@ __global__ void __launch_bounds__(W * 32, 32 / W) token_logprobs_kernel(LpArgs a
   // ---------------------------------------------------------------- one pass over the CTA's tiles
   // full tiles [b0, b1) of the CTA first, then what the row begins or ends with
   const int b0 = max(t0, tiles.head > 0 ? 1 : 0), b1 = min(t1, tiles.full_end());
+  __syncwarp();
   if (CLUSTER) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   const MaxOut<CLUSTER> out(s_max, C, lane);
   WarpSums<DT, CLUSTER> sums(a.c);
@@ -629,8 +631,8 @@ __global__ void __launch_bounds__(kLbThreads) token_logprobs_bwd_kernel(LbArgs a
 
   pdl_wait();
   pdl_trigger();
-  const int tok = __ldg(a.tokens + n);
-  const float2 st = __ldg(a.stats + n);
+  const int tok = a.tokens[n];
+  const float2 st = a.stats[n];
   if (tok < 0 || tok >= a.V || st.x == -INFINITY) {  // a row without a token or without any unmasked logit
     if (a.vec) {
       const uint4 z = make_uint4(0, 0, 0, 0);
@@ -649,19 +651,19 @@ __global__ void __launch_bounds__(kLbThreads) token_logprobs_bwd_kernel(LbArgs a
 #pragma unroll
   for (int j = 0; j < kLbVecs; ++j)
     if (j * kLbThreads + tid < nv) v[j] = q[j * kLbThreads + tid];
-  const float gl = a.g_logp ? __ldg(a.g_logp + n) : 0.f;
-  const float gH = a.g_entropy ? __ldg(a.g_entropy + n) : 0.f;
+  const float gl = a.g_logp ? a.g_logp[n] : 0.f;
+  const float gH = a.g_entropy ? a.g_entropy[n] : 0.f;
   float G = gl;
   const int32_t* ti = a.top ? a.top_idx + n * a.top : nullptr;
   const float* gt = a.top ? a.g_top + n * a.top : nullptr;
   for (int j = 0; j < a.top; ++j)
-    if ((unsigned)__ldg(ti + j) < (unsigned)a.V) G += __ldg(gt + j);
+    if ((unsigned)ti[j] < (unsigned)a.V) G += gt[j];
   LbRow r;
   r.m = st.x;
   r.s = st.y * kLog2e;
   r.c = a.c;
   r.k1 = -a.inv_T * gH * (float)kLn2D;
-  r.k0 = -a.inv_T * (gH != 0.f ? fmaf(gH, __ldg(a.entropy + n), G) : G);
+  r.k0 = -a.inv_T * (gH != 0.f ? fmaf(gH, a.entropy[n], G) : G);
   if (!(st.x < INFINITY)) r.k0 = __int_as_float(0x7FC00000);  // a row with NaN or +inf: its gradient is NaN
 
   // elements with an indicator: thread j < top + 1 owns index j if it is its first occurrence.  The
@@ -669,16 +671,16 @@ __global__ void __launch_bounds__(kLbThreads) token_logprobs_bwd_kernel(LbArgs a
   int own = -1;
   float fix = 0.f;
   if (tid <= a.top) {
-    const int idx = tid == 0 ? tok : __ldg(ti + tid - 1);
+    const int idx = tid == 0 ? tok : ti[tid - 1];
     bool first = idx >= lo && idx < hi;
     if (first && tid > 0) {
       first = idx != tok;
-      for (int j = 0; first && j < tid - 1; ++j) first = __ldg(ti + j) != idx;
+      for (int j = 0; first && j < tid - 1; ++j) first = ti[j] != idx;
     }
     if (first) {
       float add = tid == 0 ? gl : 0.f;
       for (int j = 0; j < a.top; ++j)
-        if (__ldg(ti + j) == idx) add += __ldg(gt + j);
+        if (ti[j] == idx) add += gt[j];
       own = idx;
       fix = r.dense(E::get(p[idx])) + add * a.inv_T;
     }

@@ -252,10 +252,10 @@ __global__ void __launch_bounds__(kMqThreads, 1)
       const bool mine = b < a.blocks && b * 128 + q * 32 + lane < a.bv && v < a.N;
       const int nm = min(a.bn, a.M - m0);
       // both scales before the wait: lane i holds the tokens' i, i + 32, ...
-      const float sw = mine ? __ldg(a.w_scale + v) : 0.f;
+      const float sw = mine ? a.w_scale[v] : 0.f;
       float sq[kMqMaxTokens / 32];
 #pragma unroll
-      for (int i = 0; i < kMqMaxTokens / 32; ++i) sq[i] = i * 32 + lane < nm ? __ldg(a.q_scale + m0 + i * 32 + lane) : 0.f;
+      for (int i = 0; i < kMqMaxTokens / 32; ++i) sq[i] = i * 32 + lane < nm ? a.q_scale[m0 + i * 32 + lane] : 0.f;
       const bool ok = __all_sync(0xffffffffu, mq_wait(sy, &t_full[buf], acc_r.phase));
       tc_fence_after();
       if (b < a.blocks) {
@@ -490,10 +490,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     for (int t = pair; t < a.ntiles; t += npairs, acc_r.next(2)) {
       const int buf = acc_r.s;
       const int v0 = (t / a.ntok) * 256 + (int)rank * 128, v = v0 + gt, m0 = (t % a.ntok) * a.bn;
-      const float sw = v < a.N ? __ldg(a.w_scale + v) : 0.f;
+      const float sw = v < a.N ? a.w_scale[v] : 0.f;
       const int nm = min(a.bn, a.M - m0);
       auto scale_of = [&](int c) {  // lanes 0-15: the tokens' scales of the chunk at c
-        return c + lane < nm && lane < kOutTokens ? __ldg(a.q_scale + m0 + c + lane) : 0.f;
+        return c + lane < nm && lane < kOutTokens ? a.q_scale[m0 + c + lane] : 0.f;
       };
       float sq = scale_of(h * kOutTokens);
       const bool ok = __all_sync(0xffffffffu, mq_wait(sy, &t_full[buf], acc_r.phase));

@@ -104,7 +104,7 @@ struct Gain {
   __device__ __forceinline__ void load(const void* gain, int i) {
     if (!gain) return;
 #pragma unroll
-    for (int k = 0; k < kWords; ++k) w[k] = __ldg(static_cast<const uint4*>(gain) + i * kWords + k);
+    for (int k = 0; k < kWords; ++k) w[k] = static_cast<const uint4*>(gain)[i * kWords + k];
   }
   __device__ __forceinline__ float2 pair(bool have, int i) const {
     if (!have) return make_float2(1.f, 1.f);
@@ -266,7 +266,7 @@ struct GainAt {
       uint4 t = make_uint4(0, 0, 0, 0);
       if (k < kVecs - 1 || off) {
         const int end = (i / kPer + k + 1) * kPer;  // past the vector's last gain
-        if (end <= d) t = __ldg(g + k);
+        if (end <= d) t = g[k];
         else t = partial(gain, end - kPer, d);
       }
       in[4 * k] = t.x;
