@@ -222,7 +222,8 @@ template <int DT, bool CLUSTER>
 struct WarpSums {
   using E = Elem<DT>;
   static constexpr int kPairs = E::kVec / 2, kLoads = RowTiles<DT>::kLoads;
-  static constexpr int kAhead = 1;
+  // 2 KB a warp in flight (fp32 tiles are 2 KB): with few rows of 16-bit values one 1 KB tile is too little
+  static constexpr int kAhead = DT == DSPARK_F32 ? 1 : 2;
   float c, R;
   float2 S2, E2;
   int bad;
@@ -734,7 +735,13 @@ static dspark_status launch_lp(const LogprobsCall& c) {
   // warps per CTA by the row's tiles, so that a warp has enough of them for the row's end to cost little
   // (2, 4 and 8 warps: 2000 x 12000 fp32 23.5, 24.9 and 29.8 us; 700 x 50000 fp32 38, 30.5 and 34 us;
   // 1000 x 100001 bf16 77, 61 and 57 us)
-  auto one = nt <= 32 ? launch_lp<DT, 2, false> : nt <= 128 ? launch_lp<DT, 4, false> : launch_lp<DT, 8, false>;
+  int W = nt <= 32 ? 2 : nt <= 128 ? 4 : 8;
+  // and more of them while the rows leave the SMs half empty (32 warps each)
+  while (W < 16 && 2ll * W * c.N <= 16 * slots && nt >= 4 * W) W *= 2;
+  auto one = W == 2   ? launch_lp<DT, 2, false>
+             : W == 4 ? launch_lp<DT, 4, false>
+             : W == 8 ? launch_lp<DT, 8, false>
+                      : launch_lp<DT, 16, false>;
   cudaError_t rc = C > 1 ? launch_lp<DT, 16, true>(a, c.N, C, (int)nt, c.stream) : one(a, c.N, 1, (int)nt, c.stream);
   if (rc != cudaSuccess && C > 8) {  // no clusters of 16 here
     cudaGetLastError();
