@@ -13,7 +13,7 @@
 // grows.  The sums are fp32 per lane (some 300 terms), joined pairwise over lanes, warps and CTAs; the
 // logarithm and what follows are fp64.
 // The loop costs about 6 instructions a value (packed fp32 pairs; one ex2), which at 16 bits a value is
-// near what the SM can issue while HBM streams: 1088 x 151936 fp32 takes 109 us among other calls (6.1
+// near what the SM can issue while HBM streams: 1088 x 151936 fp32 takes 104 us among other calls (6.4
 // TB/s) and 118 after a flush of L2, 2048 x 262144 bf16 188 us.  One row of 151936 with 20 alternatives
 // takes 16 us: a cluster of 16 CTAs, two cluster barriers, the choice of tiles and the candidates between
 // them.  (After a flush of L2:) CTAs of 8 warps, four to an SM, hide each other's row ends better than two of 16 (131
