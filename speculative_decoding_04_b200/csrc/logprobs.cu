@@ -10,8 +10,9 @@
 // One pass: a warp loads a tile (two or four 16-byte loads a lane, the next tile's loads in flight
 // meanwhile), reduces its maximum, keeps it in shared memory as the tile's record and adds the tile to
 // the warp's running (R, S, E) = (reference, sum 2^x, sum 2^x x), x = (l - R) log2(e)/T, rescaled when R
-// grows.  The sums are fp32 per lane (some 300 terms), joined pairwise over lanes, warps and CTAs; the
-// logarithm and what follows are fp64.
+// grows.  The sums are fp32 per lane (some 300 terms), joined pairwise over lanes, warps and CTAs, and
+// leave one maximum out of S, so that the log probability and the entropy of a row with one dominant
+// token keep their digits; the logarithm and what follows are fp64.
 // The loop costs about 6 instructions a value (packed fp32 pairs; one ex2), which at 16 bits a value is
 // near what the SM can issue while HBM streams: 1088 x 151936 fp32 takes 104 us among other calls (6.4
 // TB/s) and 118 after a flush of L2, 2048 x 262144 bf16 188 us.  One row of 151936 with 20 alternatives
@@ -106,6 +107,11 @@ struct Elem<DSPARK_F16> {
   }
 };
 
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
 __device__ __forceinline__ float ex2(float x) {
   float d;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(d) : "f"(x));
@@ -168,7 +174,9 @@ struct RowTiles {
   }
 };
 
-struct CtaPart {  // a CTA's sums against its maximum: sum 2^x and sum 2^x x
+// Sums against their maximum R: sum 2^x over all values but one that equals R (its 2^0 = 1 is left out, so
+// that small sums beside it keep their digits), and sum 2^x x.
+struct CtaPart {
   float S, E, R;
   int bad;
 };
@@ -185,11 +193,17 @@ constexpr float kFloor = -200.f;
 // Sums against different maxima joined over the lanes of a warp.
 __device__ __forceinline__ CtaPart join_parts(CtaPart p, float c) {
   const float M = redux_max(p.R);
+  const unsigned who = __ballot_sync(0xffffffffu, p.R == M);
   float S = 0.f, E = 0.f;
   if (p.R > -INFINITY) {
-    const float dr = fmaxf((p.R - M) * c, kFloor), f = exp2f(dr);
-    S = p.S * f;
-    E = fmaf(p.S, dr, p.E) * f;
+    if ((int)(threadIdx.x & 31) == __ffs(who) - 1) {  // the one value left out of the joined sum is this one's
+      S = p.S;
+      E = p.E;
+    } else {
+      const float dr = fmaxf((p.R - M) * c, kFloor), f = exp2f(dr);
+      S = fmaf(p.S, f, f);
+      E = (fmaf(p.S, dr, p.E) + dr) * f;
+    }
   }
   return CtaPart{warp_sum_f(S), warp_sum_f(E), M, __any_sync(0xffffffffu, p.bad)};
 }
@@ -230,10 +244,11 @@ struct WarpSums {
   __device__ explicit WarpSums(float c_)
       : c(c_), R(-INFINITY), S2(make_float2(0.f, 0.f)), E2(make_float2(0.f, 0.f)), bad(0) {}
 
-  // One tile into the sums; false if they are no longer numbers.  Masked values (0 * -inf in E) and NaN
-  // need CLAMP; rows without them, most, go without its two instructions a pair.
+  // One tile into the sums; false if they are no longer numbers.  Masked values (0 * -inf in E) need
+  // CLAMP; rows without them, most, go without its two instructions a pair, but for the few tiles that
+  // bring a new maximum, whose value is left out of S.
   template <bool CLAMP>
-  __device__ __forceinline__ bool tile(const uint4 (&v)[kLoads], int t, const MaxOut<CLUSTER>& out) {
+  __device__ __forceinline__ bool tile(const uint4 (&v)[kLoads], int lane, int t, const MaxOut<CLUSTER>& out) {
     float m = -INFINITY;
 #pragma unroll
     for (int j = 0; j < kLoads; ++j)
@@ -245,24 +260,53 @@ struct WarpSums {
     m = CLAMP ? warp_max_nan(m) : redux_max(m);
     out.put(t, m);
     if (CLAMP) bad |= !(m < INFINITY);  // NaN or +inf
-    if (m > R) {                        // the same for all lanes
+    const bool rise = m > R;            // the same for all lanes
+    uint32_t leave = 0;                 // this lane's value that is left out, as a bit
+    if (rise) {
       const float dr = fmaxf((R - m) * c, kFloor), f = ex2(dr);  // R = -inf: S = E = 0 stay
       E2 = p_mul(p_fma(S2, make_float2(dr, dr), E2), make_float2(f, f));
       S2 = p_mul(S2, make_float2(f, f));
+      if (lane == 0 && R > -INFINITY) {  // the value left out so far
+        S2.x += f;
+        E2.x = fmaf(dr, f, E2.x);
+      }
       R = m;
+#pragma unroll
+      for (int j = 0; j < kLoads; ++j)
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i) {
+          const float2 x = E::pair(v[j], i);
+          leave |= (x.x == m ? 1u : 0u) << (2 * (j * kPairs + i)) | (x.y == m ? 2u : 0u) << (2 * (j * kPairs + i));
+        }
+      const unsigned who = __ballot_sync(0xffffffffu, leave != 0);
+      leave = lane == __ffs(who) - 1 ? leave & -leave : 0;
     }
     if (CLAMP && R == -INFINITY) return true;
     const float2 nR = make_float2(-R, -R), c2 = make_float2(c, c);
+    if (CLAMP || rise) {
 #pragma unroll
-    for (int j = 0; j < kLoads; ++j)
+      for (int j = 0; j < kLoads; ++j)
 #pragma unroll
-      for (int i = 0; i < kPairs; ++i) {
-        float2 d = p_mul(p_add(E::pair(v[j], i), nR), c2);
-        if (CLAMP) d = make_float2(fmaxf(d.x, kFloor), fmaxf(d.y, kFloor));
-        const float2 e = make_float2(ex2(d.x), ex2(d.y));
-        S2 = p_add(S2, e);
-        E2 = p_fma(e, d, E2);
-      }
+        for (int i = 0; i < kPairs; ++i) {
+          float2 d = p_mul(p_add(E::pair(v[j], i), nR), c2);
+          d = make_float2(max_nan(d.x, kFloor), max_nan(d.y, kFloor));
+          if (leave >> (2 * (j * kPairs + i)) & 1) d.x = kFloor;
+          if (leave >> (2 * (j * kPairs + i) + 1) & 1) d.y = kFloor;
+          const float2 e = make_float2(ex2(d.x), ex2(d.y));
+          S2 = p_add(S2, e);
+          E2 = p_fma(e, d, E2);
+        }
+    } else {
+#pragma unroll
+      for (int j = 0; j < kLoads; ++j)
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i) {
+          const float2 d = p_mul(p_add(E::pair(v[j], i), nR), c2);
+          const float2 e = make_float2(ex2(d.x), ex2(d.y));
+          S2 = p_add(S2, e);
+          E2 = p_fma(e, d, E2);
+        }
+    }
     if (CLAMP) return true;
     const float x = E2.x + E2.y;
     return !__any_sync(0xffffffffu, x != x);
@@ -280,7 +324,7 @@ struct WarpSums {
       for (int u = 0; u <= kAhead; ++u)
         if (t + u * W < end) {
           fetch<W>(src, u + kAhead, t, end, buf[(u + kAhead) % (kAhead + 1)]);
-          if (!tile<CLAMP>(buf[u], t + u * W, out)) return false;
+          if (!tile<CLAMP>(buf[u], lane, t + u * W, out)) return false;
         }
       t += (kAhead + 1) * W;
       src += (kAhead + 1) * (W * 32 * kLoads);
@@ -369,12 +413,12 @@ __global__ void __launch_bounds__(W * 32, 32 / W) token_logprobs_kernel(LpArgs a
       if (t < t0 || t >= t1 || (t >= b0 && t < b1) || (e == 1 && nt == 1)) continue;
       uint4 v[kLoads];
       tiles.load_edge(tiles.start(t), tiles.end(t) - tiles.start(t), lane, v);
-      sums.template tile<true>(v, t, out);
+      sums.template tile<true>(v, lane, t, out);
     }
   }
   {
     const float S = warp_sum_f(sums.S2.x + sums.S2.y), Es = warp_sum_f(sums.E2.x + sums.E2.y);
-    if (lane == 0) s_warp[warp] = CtaPart{S, Es, sums.R, sums.bad};
+    if (lane == 0) s_warp[warp] = CtaPart{S, Es, sums.R, sums.bad | !(sums.R < INFINITY)};
   }
   __syncwarp();
   // the tiles' maxima are everywhere, and the CTA's partial sums here
@@ -498,7 +542,7 @@ __global__ void __launch_bounds__(W * 32, 32 / W) token_logprobs_kernel(LpArgs a
       if (CLUSTER) p = join_parts(lane < C ? s_part[lane] : CtaPart{0.f, 0.f, -INFINITY, 0}, a.c);
       if (lane == 0) {
         const float nan = __int_as_float(0x7FC00000);
-        double logS = log((double)p.S);
+        double logS = log1p((double)p.S);
         float lp, H, m = p.R;
         uint32_t fl = 0;
         if (p.bad) {
@@ -511,7 +555,7 @@ __global__ void __launch_bounds__(W * 32, 32 / W) token_logprobs_kernel(LpArgs a
           lp = -INFINITY;
           H = 0.f;
         } else {
-          H = (float)(logS - (double)p.E / (double)p.S * kLn2D);
+          H = (float)(logS - (double)p.E / (1.0 + (double)p.S) * kLn2D);
           lp = 0.f;
         }
         if (!in_range) {

@@ -181,6 +181,32 @@ def test_logprobs_extremes_of_magnitude():
     check(as64(t), tok, 1.0, 3, D.token_logprobs(t, dev(tok), 1.0, top=3))
 
 
+@pytest.mark.parametrize("dtype,N", [("f32", 1), ("bf16", 3), ("f32", 400)])
+@pytest.mark.parametrize("gap", [0.0, 4.0, 10.0, 18.0, 28.0])
+def test_logprobs_of_a_dominant_token_keep_their_digits(dtype, N, gap):
+    """With p close to 1, -log p and the entropy are about the sum of the other tokens' exponentials, which
+    is held apart from the dominant token's 1: its relative error is that of a sum of small terms --
+    `terms` additions and 3u |d| for each term's exponent (d below 45 nats here), ex2's and the joins' --
+    not u / (1 - p).  The entropy adds its terms' own factors d: twice that."""
+    rng = np.random.default_rng(int(gap) + N)
+    V = 20_011
+    l = rng.normal(0, 1, (N, V))
+    tok = rng.integers(0, V, N).astype(np.int32)
+    l[np.arange(N), tok] = l.max(-1) + gap
+    t = strided(l, dtype)
+    logp, ent, _, _, _ = D.token_logprobs(t, dev(tok), 1.0)
+    x = as64(t)
+    z = x - x[np.arange(N), tok][:, None]
+    e = np.exp(z)
+    e[np.arange(N), tok] = 0
+    S = e.sum(-1)
+    rel = U32 * (17 * (-(-V // 512) + 1) + 20 + 3 * 45)   # 17 values a tile at most in one accumulator
+    want = np.log1p(S)
+    assert np.all(np.abs(host(logp) + want) <= rel * want)
+    H = want - (e * z).sum(-1) / (1 + S)
+    assert np.all(np.abs(host(ent) - H) <= 2 * rel * H)
+
+
 def test_logprobs_tokens_and_rows():
     rng = np.random.default_rng(21)
     n_rows, V = 9, 2049
