@@ -35,7 +35,9 @@ constexpr int kMqKB = 128;    // bytes (= values) of a block of K: one swizzled 
 constexpr int kMqBlocks = 2;  // blocks of K per stage
 constexpr int kMqMaxStages = 8;
 constexpr uint32_t kMqSmem = 227u * 1024u;
-constexpr int kMqMaxTokens = 128;      // tokens of one single-CTA call; more than this: CTA pairs
+// Tokens of one single-CTA call; more than this: CTA pairs.  (151936 x 4096, fp32 out, one CTA a tile
+// against pairs: 40 tokens 117 and 123 us, 80 121 and 125, 100 127 and 127, 128 131 and 129.)
+constexpr int kMqMaxTokens = 128;
 
 struct MqArgs {
   const float* q_scale;
