@@ -16,11 +16,11 @@
 // The loop costs about 6 instructions a value (packed fp32 pairs; one ex2), which at 16 bits a value is
 // near what the SM can issue while HBM streams: 1088 x 151936 fp32 takes 104 us among other calls (6.4
 // TB/s) and 118 after a flush of L2, 2048 x 262144 bf16 188 us.  One row of 151936 with 20 alternatives
-// takes 16 us: a cluster of 16 CTAs, two cluster barriers, the choice of tiles and the candidates between
-// them.  (After a flush of L2:) CTAs of 8 warps, four to an SM, hide each other's row ends better than two of 16 (131
-// against 141 us); a ring filled by 16-byte asynchronous copies measured 139 us (its shared-memory
+// takes 12 us (16 after a flush): a cluster of 16 CTAs, two cluster barriers, the choice of tiles and the
+// candidates between them.  After a flush, on 1088 x 151936 fp32 unless stated: CTAs of 8 warps, four to
+// an SM, hide each other's row ends better than two of 16 (131 against 141 us); a ring filled by 16-byte asynchronous copies measured 139 us (its shared-memory
 // traffic competes with the exponentials), two or three tiles ahead 133 and 143 (fewer warps fit), and
-// rows' values clamped one by one against -inf 204 us in bf16 (hence the two forms of the loop).
+// values clamped one by one against -inf in every tile 204 us in bf16 (hence the two forms of the loop).
 //
 // Alternatives.  The main pass spends nothing on them beyond the tiles' maxima.  The k best elements
 // (value descending, index ascending) lie in the k best tiles ordered by (maximum descending, tile
@@ -236,32 +236,31 @@ template <int DT, bool CLUSTER>
 struct WarpSums {
   using E = Elem<DT>;
   static constexpr int kPairs = E::kVec / 2, kLoads = RowTiles<DT>::kLoads;
-  // 2 KB a warp in flight (fp32 tiles are 2 KB): with few rows of 16-bit values one 1 KB tile is too little
-  static constexpr int kAhead = DT == DSPARK_F32 ? 1 : 2;
+  static constexpr int kAhead = 1;  // (two in 16 bits: 213 against 188 us for 2048 x 262144 bf16, registers spill)
   float c, R;
   float2 S2, E2;
-  int bad;
+  bool clamp;
   __device__ explicit WarpSums(float c_)
-      : c(c_), R(-INFINITY), S2(make_float2(0.f, 0.f)), E2(make_float2(0.f, 0.f)), bad(0) {}
+      : c(c_), R(-INFINITY), S2(make_float2(0.f, 0.f)), E2(make_float2(0.f, 0.f)), clamp(false) {}
 
-  // One tile into the sums; false if they are no longer numbers.  Masked values (0 * -inf in E) need
-  // CLAMP; rows without them, most, go without its two instructions a pair, but for the few tiles that
-  // bring a new maximum, whose value is left out of S.
-  template <bool CLAMP>
-  __device__ __forceinline__ bool tile(const uint4 (&v)[kLoads], int lane, int t, const MaxOut<CLUSTER>& out) {
+  // One tile into the sums.  Masked values would make 0 * -inf in E, so they are clamped; that costs two
+  // instructions a pair, which rows without them, most, go without until a tile's sum shows one.  A tile
+  // that brings a new maximum takes that form too, with the maximum itself left out of S.  NaN stays in
+  // the sums.
+  __device__ __forceinline__ void tile(const uint4 (&v)[kLoads], int lane, int t, const MaxOut<CLUSTER>& out, bool edge) {
     float m = -INFINITY;
 #pragma unroll
     for (int j = 0; j < kLoads; ++j)
 #pragma unroll
       for (int i = 0; i < kPairs; ++i) {
         const float2 x = E::pair(v[j], i);
-        m = CLAMP ? max3_nan(m, x.x, x.y) : max3(m, x.x, x.y);
+        m = max3(m, x.x, x.y);
       }
-    m = CLAMP ? warp_max_nan(m) : redux_max(m);
+    m = redux_max(m);
     out.put(t, m);
-    if (CLAMP) bad |= !(m < INFINITY);  // NaN or +inf
-    const bool rise = m > R;            // the same for all lanes
-    uint32_t leave = 0;                 // this lane's value that is left out, as a bit
+    const bool rise = m > R;  // the same for all lanes
+    if (R == -INFINITY && m == -INFINITY) return;
+    uint32_t leave = 0;  // this lane's value that is left out, as a bit
     if (rise) {
       const float dr = fmaxf((R - m) * c, kFloor), f = ex2(dr);  // R = -inf: S = E = 0 stay
       E2 = p_mul(p_fma(S2, make_float2(dr, dr), E2), make_float2(f, f));
@@ -281,9 +280,27 @@ struct WarpSums {
       const unsigned who = __ballot_sync(0xffffffffu, leave != 0);
       leave = lane == __ffs(who) - 1 ? leave & -leave : 0;
     }
-    if (CLAMP && R == -INFINITY) return true;
     const float2 nR = make_float2(-R, -R), c2 = make_float2(c, c);
-    if (CLAMP || rise) {
+    float2 ts = make_float2(0.f, 0.f), te = make_float2(0.f, 0.f);
+    bool slow = clamp || rise || edge;
+    if (!slow) {
+#pragma unroll
+      for (int j = 0; j < kLoads; ++j)
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i) {
+          const float2 d = p_mul(p_add(E::pair(v[j], i), nR), c2);
+          const float2 e = make_float2(ex2(d.x), ex2(d.y));
+          ts = p_add(ts, e);
+          te = p_fma(e, d, te);
+        }
+      const float x = te.x + te.y;
+      slow = __any_sync(0xffffffffu, x != x);
+      if (slow) {
+        clamp = true;
+        ts = te = make_float2(0.f, 0.f);
+      }
+    }
+    if (slow) {
 #pragma unroll
       for (int j = 0; j < kLoads; ++j)
 #pragma unroll
@@ -293,28 +310,17 @@ struct WarpSums {
           if (leave >> (2 * (j * kPairs + i)) & 1) d.x = kFloor;
           if (leave >> (2 * (j * kPairs + i) + 1) & 1) d.y = kFloor;
           const float2 e = make_float2(ex2(d.x), ex2(d.y));
-          S2 = p_add(S2, e);
-          E2 = p_fma(e, d, E2);
-        }
-    } else {
-#pragma unroll
-      for (int j = 0; j < kLoads; ++j)
-#pragma unroll
-        for (int i = 0; i < kPairs; ++i) {
-          const float2 d = p_mul(p_add(E::pair(v[j], i), nR), c2);
-          const float2 e = make_float2(ex2(d.x), ex2(d.y));
-          S2 = p_add(S2, e);
-          E2 = p_fma(e, d, E2);
+          ts = p_add(ts, e);
+          te = p_fma(e, d, te);
         }
     }
-    if (CLAMP) return true;
-    const float x = E2.x + E2.y;
-    return !__any_sync(0xffffffffu, x != x);
+    S2 = p_add(S2, ts);
+    E2 = p_add(E2, te);
   }
 
-  // Full tiles t, t + W, ... below end, the next kAhead tiles' loads in flight; false as tile().
-  template <bool CLAMP, int W>
-  __device__ __forceinline__ bool pass(const RowTiles<DT>& tiles, int t, int end, int lane, const MaxOut<CLUSTER>& out) {
+  // Full tiles t, t + W, ... below end, the next kAhead tiles' loads in flight.
+  template <int W>
+  __device__ __forceinline__ void pass(const RowTiles<DT>& tiles, int t, int end, int lane, const MaxOut<CLUSTER>& out) {
     const uint4* src = reinterpret_cast<const uint4*>(tiles.p + tiles.start(t)) + lane;
     uint4 buf[kAhead + 1][kLoads];
 #pragma unroll
@@ -324,12 +330,11 @@ struct WarpSums {
       for (int u = 0; u <= kAhead; ++u)
         if (t + u * W < end) {
           fetch<W>(src, u + kAhead, t, end, buf[(u + kAhead) % (kAhead + 1)]);
-          if (!tile<CLAMP>(buf[u], lane, t + u * W, out)) return false;
+          tile(buf[u], lane, t + u * W, out, false);
         }
       t += (kAhead + 1) * W;
       src += (kAhead + 1) * (W * 32 * kLoads);
     }
-    return true;
   }
   template <int W>
   static __device__ __forceinline__ void fetch(const uint4* src, int i, int t, int end, uint4 (&v)[kLoads]) {
@@ -403,22 +408,19 @@ __global__ void __launch_bounds__(W * 32, 32 / W) token_logprobs_kernel(LpArgs a
   if (CLUSTER) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   const MaxOut<CLUSTER> out(s_max, C, lane);
   WarpSums<DT, CLUSTER> sums(a.c);
-  if (!sums.template pass<false, W>(tiles, b0 + warp, b1, lane, out)) {
-    sums = WarpSums<DT, CLUSTER>(a.c);
-    sums.template pass<true, W>(tiles, b0 + warp, b1, lane, out);
-  }
+  sums.template pass<W>(tiles, b0 + warp, b1, lane, out);
   if (warp == W - 1) {
     for (int e = 0; e < 2; ++e) {
       const int t = e == 0 ? 0 : nt - 1;
       if (t < t0 || t >= t1 || (t >= b0 && t < b1) || (e == 1 && nt == 1)) continue;
       uint4 v[kLoads];
       tiles.load_edge(tiles.start(t), tiles.end(t) - tiles.start(t), lane, v);
-      sums.template tile<true>(v, lane, t, out);
+      sums.tile(v, lane, t, out, true);
     }
   }
   {
     const float S = warp_sum_f(sums.S2.x + sums.S2.y), Es = warp_sum_f(sums.E2.x + sums.E2.y);
-    if (lane == 0) s_warp[warp] = CtaPart{S, Es, sums.R, sums.bad | !(sums.R < INFINITY)};
+    if (lane == 0) s_warp[warp] = CtaPart{S, Es, sums.R, !(sums.R < INFINITY) || S != S || Es != Es};  // +inf or NaN
   }
   __syncwarp();
   // the tiles' maxima are everywhere, and the CTA's partial sums here
