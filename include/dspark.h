@@ -512,7 +512,8 @@ int dspark_quantize_q8(const void* x, int dtype, int64_t ldx, int M, int d, int8
  *
  * q        [M, K] int8, 16-byte aligned, rows ldq bytes apart;  q_scale [M] fp32.
  * w        [N, K] int8, 16-byte aligned, rows ldw bytes apart;  w_scale [N] fp32.
- *          ldq and ldw are multiples of 16 (bytes between a row's end and the next are not read).
+ *          ldq and ldw are multiples of 16 (bytes between a row's end and the next are not read);
+ *          multiples of 128 are read fastest.
  * out      [M, N] of out_dtype (DSPARK_F32, DSPARK_BF16 or DSPARK_F16), rows ldo elements apart.
  * flags    [M] uint32 or NULL: DEVICE_TIMEOUT where a bounded device wait gave up; the outputs it
  *          could not compute are then NaN.

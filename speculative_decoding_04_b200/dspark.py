@@ -522,7 +522,7 @@ def rmsnorm_q8(x: torch.Tensor, gain: Optional[torch.Tensor], eps: float, *, res
     """Root-mean-square norm of the rows of x (+ residual), as int8 with one scale per row.
 
     x, residual [..., d] (fp32, bf16 or fp16; rows a constant stride apart), gain [d] (x's dtype, fp32,
-    or None).  Returns (q [..., d] int8 with rows on 16 bytes, scale [...] fp32, h = x + residual in
+    or None).  Returns (q [..., d] int8 with rows on 16 bytes -- on 128 from d = 512 on --, scale [...] fp32, h = x + residual in
     x's dtype, or None without a residual): q * scale is the normalised row.  h_out may be x or the
     residual."""
     if stream is not None:

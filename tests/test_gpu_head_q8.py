@@ -199,6 +199,15 @@ def test_streams_and_graphs():
         assert all(torch.equal(a, b) for a, b in zip(want, got))
 
 
+def test_quantised_rows_are_laid_out_for_the_product():
+    for d, ld in ((100, 112), (511, 512), (512, 512), (513, 640), (4271, 4352)):
+        q, s = D.quantize_q8(torch.randn(6, d, device="cuda"))
+        assert q.shape == (6, d) and q.stride() == (ld, 1)
+        n, s2, _ = D.rmsnorm_q8(torch.randn(2, 3, d, device="cuda"), None, 1e-6)
+        assert n.shape == (2, 3, d) and n.stride() == (3 * ld, ld, 1)
+        check_matmul(n.reshape(6, d), s2.view(-1), q, s, D.matmul_q8(n, s2, q, s), "f32")
+
+
 def test_two_calls_at_once():
     """Two products on two streams: no scratch is shared."""
     rng = np.random.default_rng(12)
