@@ -13,7 +13,7 @@
 // grows.  The sums are fp32 per lane (some 300 terms), joined pairwise over lanes, warps and CTAs, and
 // leave one maximum out of S, so that the log probability and the entropy of a row with one dominant
 // token keep their digits; the logarithm and what follows are fp64.
-// The loop costs about 6 instructions a value (packed fp32 pairs; one ex2), which at 16 bits a value is
+// The loop costs under 9 instructions a value (packed fp32 pairs; one ex2), which at 16 bits a value is
 // near what the SM can issue while HBM streams: 1088 x 151936 fp32 takes 104 us among other calls (6.4
 // TB/s) and 118 after a flush of L2, 2048 x 262144 bf16 188 us.  One row of 151936 with 20 alternatives
 // takes 12 us (16 after a flush): a cluster of 16 CTAs, two cluster barriers, the choice of tiles and the
