@@ -10,17 +10,19 @@
 // One pass: a warp loads a tile (two or four 16-byte loads a lane, the next tile's loads in flight
 // meanwhile), reduces its maximum, keeps it in shared memory as the tile's record and adds the tile to
 // the warp's running (R, S, E) = (reference, sum 2^x, sum 2^x x), x = (l - R) log2(e)/T, rescaled when R
-// grows.  The sums are fp32 per lane (some 300 terms), joined pairwise over lanes, warps and CTAs, and
-// leave one maximum out of S, so that the log probability and the entropy of a row with one dominant
-// token keep their digits; the logarithm and what follows are fp64.
+// grows (in a branch of its own: 47 against 49 us at 944 x 77028 bf16).  The sums are fp32 per lane (per
+// tile, then over the tiles), joined pairwise over lanes, warps and CTAs, and leave one maximum out of S,
+// so that the log probability and the entropy of a row with one dominant token keep their digits; the
+// logarithm and what follows are fp64.
 // The loop costs under 9 instructions a value (packed fp32 pairs; one ex2), which at 16 bits a value is
 // near what the SM can issue while HBM streams: 1088 x 151936 fp32 takes 104 us among other calls (6.4
-// TB/s) and 118 after a flush of L2, 2048 x 262144 bf16 188 us.  One row of 151936 with 20 alternatives
+// TB/s) and 118 after a flush of L2, 2048 x 262144 bf16 183 us.  One row of 151936 with 20 alternatives
 // takes 12 us (16 after a flush): a cluster of 16 CTAs, two cluster barriers, the choice of tiles and the
 // candidates between them.  After a flush, on 1088 x 151936 fp32 unless stated: CTAs of 8 warps, four to
-// an SM, hide each other's row ends better than two of 16 (131 against 141 us); a ring filled by 16-byte asynchronous copies measured 139 us (its shared-memory
-// traffic competes with the exponentials), two or three tiles ahead 133 and 143 (fewer warps fit), and
-// values clamped one by one against -inf in every tile 204 us in bf16 (hence the two forms of the loop).
+// an SM, hide each other's row ends better than two of 16 (131 against 141 us); a ring filled by 16-byte
+// asynchronous copies measured 139 us (its shared-memory traffic competes with the exponentials), two or
+// three tiles ahead 133 and 143 (fewer warps fit), and values clamped one by one against -inf in every
+// tile 204 us at 2048 x 262144 bf16 (hence the two forms of the loop).
 //
 // Alternatives.  The main pass spends nothing on them beyond the tiles' maxima.  The k best elements
 // (value descending, index ascending) lie in the k best tiles ordered by (maximum descending, tile
@@ -248,20 +250,17 @@ struct WarpSums {
   // that brings a new maximum takes that form too, with the maximum itself left out of S.  NaN stays in
   // the sums.
   __device__ __forceinline__ void tile(const uint4 (&v)[kLoads], int lane, int t, const MaxOut<CLUSTER>& out, bool edge) {
-    float m = -INFINITY;
+    float lm = -INFINITY;
 #pragma unroll
     for (int j = 0; j < kLoads; ++j)
 #pragma unroll
       for (int i = 0; i < kPairs; ++i) {
         const float2 x = E::pair(v[j], i);
-        m = max3(m, x.x, x.y);
+        lm = max3(lm, x.x, x.y);
       }
-    m = redux_max(m);
+    const float m = redux_max(lm);
     out.put(t, m);
-    const bool rise = m > R;  // the same for all lanes
-    if (R == -INFINITY && m == -INFINITY) return;
-    uint32_t leave = 0;  // this lane's value that is left out, as a bit
-    if (rise) {
+    if (m > R) {  // the same for all lanes
       const float dr = fmaxf((R - m) * c, kFloor), f = ex2(dr);  // R = -inf: S = E = 0 stay
       E2 = p_mul(p_fma(S2, make_float2(dr, dr), E2), make_float2(f, f));
       S2 = p_mul(S2, make_float2(f, f));
@@ -270,50 +269,67 @@ struct WarpSums {
         E2.x = fmaf(dr, f, E2.x);
       }
       R = m;
+      bool leave = lane == __ffs(__ballot_sync(0xffffffffu, lm == m)) - 1;  // this lane's first value m is left out
+      const float2 nR = make_float2(-R, -R), c2 = make_float2(c, c);
+      float2 ts, te;
 #pragma unroll
       for (int j = 0; j < kLoads; ++j)
 #pragma unroll
         for (int i = 0; i < kPairs; ++i) {
           const float2 x = E::pair(v[j], i);
-          leave |= (x.x == m ? 1u : 0u) << (2 * (j * kPairs + i)) | (x.y == m ? 2u : 0u) << (2 * (j * kPairs + i));
+          float2 d = p_mul(p_add(x, nR), c2);
+          d = make_float2(max_nan(d.x, kFloor), max_nan(d.y, kFloor));
+          if (leave && x.x == m) {
+            d.x = kFloor;
+            leave = false;
+          }
+          if (leave && x.y == m) {
+            d.y = kFloor;
+            leave = false;
+          }
+          const float2 e = make_float2(ex2(d.x), ex2(d.y));
+          const bool first = j == 0 && i == 0;
+          ts = first ? e : p_add(ts, e);
+          te = first ? p_mul(e, d) : p_fma(e, d, te);
         }
-      const unsigned who = __ballot_sync(0xffffffffu, leave != 0);
-      leave = lane == __ffs(who) - 1 ? leave & -leave : 0;
+      S2 = p_add(S2, ts);
+      E2 = p_add(E2, te);
+      return;
     }
     const float2 nR = make_float2(-R, -R), c2 = make_float2(c, c);
-    float2 ts = make_float2(0.f, 0.f), te = make_float2(0.f, 0.f);
-    bool slow = clamp || rise || edge;
-    if (!slow) {
+    if (!clamp && !edge) {
+      float2 ts, te;  // the tile's own sums: shorter chains of additions
 #pragma unroll
       for (int j = 0; j < kLoads; ++j)
 #pragma unroll
         for (int i = 0; i < kPairs; ++i) {
           const float2 d = p_mul(p_add(E::pair(v[j], i), nR), c2);
           const float2 e = make_float2(ex2(d.x), ex2(d.y));
-          ts = p_add(ts, e);
-          te = p_fma(e, d, te);
+          const bool first = j == 0 && i == 0;
+          ts = first ? e : p_add(ts, e);
+          te = first ? p_mul(e, d) : p_fma(e, d, te);
         }
       const float x = te.x + te.y;
-      slow = __any_sync(0xffffffffu, x != x);
-      if (slow) {
-        clamp = true;
-        ts = te = make_float2(0.f, 0.f);
+      if (!__any_sync(0xffffffffu, x != x)) {
+        S2 = p_add(S2, ts);
+        E2 = p_add(E2, te);
+        return;
       }
+      clamp = true;
     }
-    if (slow) {
+    if (R == -INFINITY && m == -INFINITY) return;  // nothing unmasked so far
+    float2 ts, te;
 #pragma unroll
-      for (int j = 0; j < kLoads; ++j)
+    for (int j = 0; j < kLoads; ++j)
 #pragma unroll
-        for (int i = 0; i < kPairs; ++i) {
-          float2 d = p_mul(p_add(E::pair(v[j], i), nR), c2);
-          d = make_float2(max_nan(d.x, kFloor), max_nan(d.y, kFloor));
-          if (leave >> (2 * (j * kPairs + i)) & 1) d.x = kFloor;
-          if (leave >> (2 * (j * kPairs + i) + 1) & 1) d.y = kFloor;
-          const float2 e = make_float2(ex2(d.x), ex2(d.y));
-          ts = p_add(ts, e);
-          te = p_fma(e, d, te);
-        }
-    }
+      for (int i = 0; i < kPairs; ++i) {
+        float2 d = p_mul(p_add(E::pair(v[j], i), nR), c2);
+        d = make_float2(max_nan(d.x, kFloor), max_nan(d.y, kFloor));
+        const float2 e = make_float2(ex2(d.x), ex2(d.y));
+        const bool first = j == 0 && i == 0;
+        ts = first ? e : p_add(ts, e);
+        te = first ? p_mul(e, d) : p_fma(e, d, te);
+      }
     S2 = p_add(S2, ts);
     E2 = p_add(E2, te);
   }
