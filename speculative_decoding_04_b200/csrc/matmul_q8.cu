@@ -575,26 +575,6 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 }
 
 template <int DT>
-static cudaError_t launch_pair(const MqMaps& tm, const MqArgs& a, int grid, size_t smem,
-                               cudaStream_t st) {
-  auto kern = matmul_q8_pair<DT>;
-  cudaError_t rc = ensure_smem_attr((const void*)kern, smem);
-  if (rc != cudaSuccess) return rc;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(kPairThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = 2;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, tm, a);
-}
-
-template <int DT>
 static cudaError_t launch_mq(const MqParams& p, bool pair, int grid, size_t smem, cudaStream_t st) {
   auto kern = pair ? matmul_q8_pair<DT> : matmul_q8_kernel<DT>;
   const cudaError_t rc = ensure_smem_attr((const void*)kern, smem);
