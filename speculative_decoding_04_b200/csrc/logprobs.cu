@@ -745,7 +745,12 @@ __global__ void __launch_bounds__(kLbThreads) token_logprobs_bwd_kernel(LbArgs a
       for (int j = 0; j < a.top; ++j)
         if (ti[j] == idx) add += gt[j];
       own = idx;
-      fix = r.dense(E::get(p[idx])) + add * a.inv_T;
+      const float x = E::get(p[idx]), lp2 = fmaf(x - r.m, r.c, -r.s), pr = ex2(lp2);
+      if (pr > 0.5f)  // 1 - p from log p, so that a dominant token's gradient keeps its digits
+        fix = a.inv_T * ((add - G) - G * expm1f(lp2 * (float)kLn2D) -
+                         (gH != 0.f ? pr * gH * fmaf(lp2, (float)kLn2D, a.entropy[n]) : 0.f));
+      else
+        fix = r.dense(x) + add * a.inv_T;
     }
   }
   __syncthreads();

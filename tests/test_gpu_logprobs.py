@@ -340,6 +340,30 @@ def test_backward_of_the_types_lowest_value():
     assert np.allclose(host(g)[0], want, rtol=64 * U32, atol=0)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("gap", [2.0, 10.0, 25.0])
+def test_backward_of_a_dominant_token_keeps_its_digits(dtype, gap):
+    """g (1 - p) of a token with p close to 1: 1 - p comes from log p, whose relative error is that of the
+    sum of the other tokens' exponentials (as for the forward call), passed on by a factor of at most 1, and
+    some 12 roundings follow."""
+    rng = np.random.default_rng(int(gap))
+    N, V, T = 5, 20_011, 1.0
+    l = rng.normal(0, 1, (N, V))
+    tok = rng.integers(0, V, N).astype(np.int32)
+    l[np.arange(N), tok] = l.max(-1) + gap
+    t = strided(l, dtype)
+    _, ent, _, _, st = D.token_logprobs(t, dev(tok), T)
+    gl = rng.normal(size=N).astype(np.float32)
+    g = D.token_logprobs_backward(t, dev(tok), T, st, ent, dev(gl)).double().cpu().numpy()[np.arange(N), tok]
+    x = as64(t)
+    e = np.exp(x - x[np.arange(N), tok][:, None])
+    e[np.arange(N), tok] = 0
+    S = e.sum(-1)
+    want = gl * S / (1 + S)
+    rel = U32 * (17 * (-(-V // 512) + 1) + 20 + 3 * 45 + 12)
+    assert np.all(np.abs(g - want) <= (rel + EPS[dtype] * (1 + 1e-3)) * np.abs(want))
+
+
 def test_backward_by_differences():
     """The gradient against central differences of the forward kernel itself: with h = 2^-3 the
     difference quotient of logp (fp32, error below 2e-5 of 10) is good to 2e-5 * 10 / h and the third
