@@ -481,7 +481,7 @@ int dspark_token_logprobs_backward(const void* logits, int dtype, int64_t ld, co
  * x         [M, d] of dtype (DSPARK_F32, DSPARK_BF16 or DSPARK_F16), rows ldx elements apart.
  * residual  [M, d] of dtype, rows ldr apart, or NULL.
  * gain      [d] of gain_dtype (dtype itself or DSPARK_F32), or NULL (1).
- * eps       > 0, finite.
+ * eps       >= 2^-100, finite.
  * h_out     [M, d] of dtype, rows ldh apart: required with a residual, ignored without.  It may be x
  *           or the residual itself (same address and stride).
  * q         [M, d] int8, rows ldq bytes apart (a multiple of 16 for dspark_matmul_q8).

@@ -378,7 +378,8 @@ int dspark_rmsnorm_q8(const void* x, int dtype, int64_t ldx, const void* residua
   if (M < 0 || d < 1) return einval("dspark_rmsnorm_q8: M must be >= 0 and d >= 1");
   if (ldx < d || ldq < d || (residual && (ldr < d || ldh < d)))
     return einval("dspark_rmsnorm_q8: row strides must be >= d");
-  if (!(eps > 0.f) || std::isinf(eps)) return einval("dspark_rmsnorm_q8: eps must be finite and > 0");
+  // (smaller ones would be compared with squares that fp32 holds as denormals)
+  if (!(eps >= 0x1p-100f) || std::isinf(eps)) return einval("dspark_rmsnorm_q8: eps must be finite and >= 2^-100");
   if (M == 0) return DSPARK_OK;
   if (!x || !q || !scale || (residual && !h_out)) return einval("dspark_rmsnorm_q8: null pointer");
   if ((uintptr_t)x % es || (uintptr_t)residual % es || (residual && (uintptr_t)h_out % es) ||

@@ -484,6 +484,16 @@ def prefix_schedule_t2(c: torch.Tensor, sps: torch.Tensor, D_max: int, ring: tor
     return L_out, a_out, theta_out, K_out, flags
 
 
+def _call(f, stream, first: torch.Tensor, *args):
+    # f of the extension module on `stream`, or on the current stream of the first tensor's device
+    if stream is None:
+        return f(first, *args)
+    if stream.device != first.device:
+        raise ValueError("stream is on another device than the tensors")
+    with torch.cuda.stream(stream):
+        return f(first, *args)
+
+
 def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, T: float = 1.0, *, top: int = 0, rows=None, logp=None,
                    entropy=None, top_idx=None, top_logp=None, stats=None, flags=None, stream=None):
     """Log probabilities of `tokens` under rows of `logits` at temperature T, with entropy and the
@@ -494,10 +504,8 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, T: float = 1.0, *
     as tokens).  -1 is an entry without a token.  Returns (logp, entropy, top_idx, top_logp, stats):
     logp and entropy shaped as tokens, the alternatives [..., top] (None when top is 0), stats [..., 2]
     for token_logprobs_backward.  flags: int32, one word per entry, zeroed by the caller, or None."""
-    if stream is not None:
-        with torch.cuda.stream(stream):
-            return _binding.token_logprobs(logits, tokens, T, top, rows, logp, entropy, top_idx, top_logp, stats, flags)
-    return _binding.token_logprobs(logits, tokens, T, top, rows, logp, entropy, top_idx, top_logp, stats, flags)
+    return _call(_binding.token_logprobs, stream, logits, tokens, T, top, rows, logp, entropy, top_idx, top_logp, stats,
+                 flags)
 
 
 def token_logprobs_backward(logits: torch.Tensor, tokens: torch.Tensor, T: float, stats: torch.Tensor,
@@ -510,11 +518,8 @@ def token_logprobs_backward(logits: torch.Tensor, tokens: torch.Tensor, T: float
     forward's top_idx): the gradients of its outputs, each or None.  grad: where to write it -- the
     logits' dtype and shape, the logits themselves among them -- or None: a new tensor with the strides
     of the logits' rows."""
-    if stream is not None:
-        with torch.cuda.stream(stream):
-            return _binding.token_logprobs_backward(logits, tokens, T, stats, entropy, g_logp, g_entropy, top_idx, g_top,
-                                                    grad)
-    return _binding.token_logprobs_backward(logits, tokens, T, stats, entropy, g_logp, g_entropy, top_idx, g_top, grad)
+    return _call(_binding.token_logprobs_backward, stream, logits, tokens, T, stats, entropy, g_logp, g_entropy, top_idx,
+                 g_top, grad)
 
 
 def rmsnorm_q8(x: torch.Tensor, gain: Optional[torch.Tensor], eps: float, *, residual: Optional[torch.Tensor] = None,
@@ -522,21 +527,15 @@ def rmsnorm_q8(x: torch.Tensor, gain: Optional[torch.Tensor], eps: float, *, res
     """Root-mean-square norm of the rows of x (+ residual), as int8 with one scale per row.
 
     x, residual [..., d] (fp32, bf16 or fp16; rows a constant stride apart), gain [d] (x's dtype, fp32,
-    or None).  Returns (q [..., d] int8 with rows on 16 bytes -- on 128 from d = 512 on --, scale [...] fp32, h = x + residual in
-    x's dtype, or None without a residual): q * scale is the normalised row.  h_out may be x or the
-    residual."""
-    if stream is not None:
-        with torch.cuda.stream(stream):
-            return _binding.rmsnorm_q8(x, gain, eps, residual, h_out, q, scale)
-    return _binding.rmsnorm_q8(x, gain, eps, residual, h_out, q, scale)
+    or None), eps >= 2^-100.  Returns (q [..., d] int8 with rows on 16 bytes -- on 128 from d = 512 on --,
+    scale [...] fp32, h = x + residual in x's dtype, or None without a residual): q * scale is the
+    normalised row.  h_out may be x or the residual."""
+    return _call(_binding.rmsnorm_q8, stream, x, gain, eps, residual, h_out, q, scale)
 
 
 def quantize_q8(x: torch.Tensor, *, q=None, scale=None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """The rows of x [..., d] as int8 with one scale per row: (q, scale), x about q * scale."""
-    if stream is not None:
-        with torch.cuda.stream(stream):
-            return _binding.quantize_q8(x, q, scale)
-    return _binding.quantize_q8(x, q, scale)
+    return _call(_binding.quantize_q8, stream, x, q, scale)
 
 
 def matmul_q8(q: torch.Tensor, q_scale: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor, *,
@@ -546,7 +545,4 @@ def matmul_q8(q: torch.Tensor, q_scale: torch.Tensor, w: torch.Tensor, w_scale: 
     q [..., K] and w [N, K] int8 with rows on 16 bytes (as rmsnorm_q8 and quantize_q8 make them), the
     scales fp32 with one value per row.  out: [..., N] in out_dtype (fp32, bf16 or fp16), or None: a new
     tensor.  With q in the order of U or l_t an fp32 result feeds markov_draft or verify."""
-    if stream is not None:
-        with torch.cuda.stream(stream):
-            return _binding.matmul_q8(q, q_scale, w, w_scale, out_dtype, out, flags)
-    return _binding.matmul_q8(q, q_scale, w, w_scale, out_dtype, out, flags)
+    return _call(_binding.matmul_q8, stream, q, q_scale, w, w_scale, out_dtype, out, flags)

@@ -118,3 +118,21 @@ def test_binding_refuses_cpu_tensors():
             f()
     with pytest.raises(TypeError):
         D.token_logprobs(x.numpy(), tok)
+
+
+@no_gpu
+def test_rmsnorm_q8_refuses_an_eps_among_the_denormals():
+    assert call("dspark_rmsnorm_q8", NQ, eps=1e-38) == D.EINVAL and "eps" in D.last_error()
+
+
+def test_a_stream_of_another_device_is_refused():
+    class Stream:
+        device = torch.device("cuda:1")
+    x = torch.zeros((4, 64))
+    i8 = torch.zeros((4, 64), dtype=torch.int8)
+    tok = torch.zeros(4, dtype=torch.int32)
+    for f in (lambda **k: D.token_logprobs(x, tok, **k), lambda **k: D.rmsnorm_q8(x, None, 1e-6, **k),
+              lambda **k: D.quantize_q8(x, **k), lambda **k: D.matmul_q8(i8, x[:, 0], i8, x[:, 0], **k),
+              lambda **k: D.token_logprobs_backward(x, tok, 1.0, x[:, :2], None, x[:, 0], **k)):
+        with pytest.raises(ValueError, match="stream"):
+            f(stream=Stream())
