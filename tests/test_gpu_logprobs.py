@@ -168,6 +168,25 @@ def test_logprobs_ties_and_orders(dtype, N):
         check(as64(t), tok, 1.0, 32, got)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("N", [1, 150])
+@pytest.mark.parametrize("top", [1, 20, 32])
+def test_logprobs_large_values_in_every_few_tiles(dtype, N, top):
+    """Rows whose large values lie in all tiles of 512 but those of every 32nd group onwards (the worst
+    spread for a choice by lanes), in one tile of 32 only, and the same value in all tiles."""
+    rng = np.random.default_rng(top)
+    V = 300_000
+    tile = np.arange(V) // 512
+    l = rng.normal(0, 1, (N, V)).astype(np.float32)
+    l[0] += np.where(tile % 32 < top - 1, 12.0, 0.0)
+    for n in range(1, min(N, 4)):
+        l[n] += [0.0, np.where(tile % 32 == 5, 12.0, 0.0), np.where(tile % 32 == 31, -30.0, 0.0),
+                 np.where(np.arange(V) % 512 == 77, 40.0 - l[n], 0.0)][n]
+    t = strided(l, dtype)
+    tok = rng.integers(0, V, N).astype(np.int32)
+    check(as64(t), tok, 0.9, top, D.token_logprobs(t, dev(tok), 0.9, top=top))
+
+
 def test_logprobs_extremes_of_magnitude():
     V = 3000
     rng = np.random.default_rng(8)
