@@ -15,10 +15,10 @@
 // so that the log probability and the entropy of a row with one dominant token keep their digits; the
 // logarithm and what follows are fp64.
 // The loop costs under 9 instructions a value (packed fp32 pairs; one ex2), which at 16 bits a value is
-// near what the SM can issue while HBM streams: 1088 x 151936 fp32 takes 104 us among other calls (6.4
-// TB/s) and 118 after a flush of L2, 2048 x 262144 bf16 183 us.  One row of 151936 with 20 alternatives
-// takes 12 us (16 after a flush): a cluster of 16 CTAs, two cluster barriers, the choice of tiles and the
-// candidates between them.  After a flush, on 1088 x 151936 fp32 unless stated: CTAs of 8 warps, four to
+// near what the SM can issue while HBM streams: 1088 x 151936 fp32 takes 102 us among other calls (6.5
+// TB/s), 2048 x 262144 bf16 183 us.  One row of 151936 takes 4.7 us without and 7.6 with 20 alternatives:
+// a cluster of 16 CTAs, two cluster barriers, the choice of tiles and the candidates between them.
+// After a flush of L2, on 1088 x 151936 fp32 unless stated, while this was built: CTAs of 8 warps, four to
 // an SM, hide each other's row ends better than two of 16 (131 against 141 us); a ring filled by 16-byte
 // asynchronous copies measured 139 us (its shared-memory traffic competes with the exponentials), two or
 // three tiles ahead 133 and 143 (fewer warps fit), and values clamped one by one against -inf in every
@@ -862,16 +862,16 @@ static dspark_status launch_lp(const LogprobsCall& c) {
   const long long nt = ((long long)c.V + kTile - 1) / kTile + 1;
   // CTAs per row: while the rows alone leave SMs idle (two CTAs of 16 warps per SM), split rows of at
   // least 8 tiles a warp, down to one tile a warp (at most 1, 2, 4, 8 and 16 CTAs: one row of 151936 fp32
-  // with 20 alternatives 18.5, 15.6, 13.6, 12.3 and 11.8 us; 64 rows 17.3, 14.7, 13.7, 13.6; 77 rows of
-  // 50001 fp16, 6 tiles a warp, 9.7 by one CTA each and 11.3 by two)
+  // with 20 alternatives 13.9, 10.4, 8.7, 7.8 and 7.6 us; 64 rows with 8 16.6, 13.5 and 12.8; 77 rows of
+  // 50001 fp16, 6 tiles a warp, 8.4 by one CTA each and 10.1 by two)
   const long long slots = 2ll * device_sm_count();
   int C = 1;
   while (C < kLpMaxCluster && (long long)c.N * 2 * C <= slots && nt >= 128 && nt / (2 * C) >= 16) C *= 2;
   LpArgs a{c.logits, c.ld, c.rows, c.n_rows, c.tokens, c.V, c.top, 1.0 / (double)c.T, (float)(1.0 / (kLn2D * (double)c.T)),
            c.logp, c.entropy, c.top_idx, c.top_logp, reinterpret_cast<float2*>(c.stats), c.flags};
   // warps per CTA by the row's tiles, so that a warp has enough of them for the row's end to cost little
-  // (2, 4 and 8 warps: 2000 x 12000 fp32 23.5, 24.9 and 29.8 us; 700 x 50000 fp32 38, 30.5 and 34 us;
-  // 1000 x 100001 bf16 77, 61 and 57 us)
+  // (2, 4 and 8 warps: 2000 x 12000 fp32 21.3, 23.3 and 28.7 us; 700 x 50000 fp32 38, 28.8 and 34 us;
+  // 1000 x 100001 bf16 63, 51 and 46 us)
   int W = nt <= 32 ? 2 : nt <= 128 ? 4 : 8;
   // and more of them while the rows leave the SMs half empty (32 warps each)
   while (W < 16 && 2ll * W * c.N <= 16 * slots && nt >= 4 * W) W *= 2;
