@@ -75,8 +75,9 @@ def build_binding(verbose=False):
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-DTORCH_EXTENSION_NAME=_binding",
            "-DTORCH_API_INCLUDE_EXTENSION_H", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
     cmd += ["-isystem" + d for d in inc] + [BINDING_SRC, "-o", tmp, "-L" + LIB_DIR, "-l:libdspark.so",
-                                            "-L" + os.path.join(torch_dir, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu",
-                                            "-ltorch", "-ltorch_python", "-Wl,-rpath,$ORIGIN"]
+                                            "-L" + os.path.join(torch_dir, "lib"), "-lc10", "-lc10_cuda",
+                                            "-ltorch_cpu", "-ltorch_cuda", "-ltorch", "-ltorch_python",
+                                            "-Wl,-rpath,$ORIGIN"]
     run(cmd, "the torch binding", verbose)
     os.replace(tmp, BINDING_PATH)
 
