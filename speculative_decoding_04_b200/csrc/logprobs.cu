@@ -14,15 +14,16 @@
 // tile, then over the tiles), joined pairwise over lanes, warps and CTAs, and leave one maximum out of S,
 // so that the log probability and the entropy of a row with one dominant token keep their digits; the
 // logarithm and what follows are fp64.
-// The loop costs under 9 instructions a value (packed fp32 pairs; one ex2), which at 16 bits a value is
-// near what the SM can issue while HBM streams: 1088 x 151936 fp32 takes 102 us among other calls (6.5
+// A value costs 8.6 instructions in fp32 and 7.3 in bf16 (packed fp32 pairs; one ex2), which at 16 bits a
+// value keeps the SM about as busy as HBM: 1088 x 151936 fp32 takes 102 us among other calls (6.5
 // TB/s), 2048 x 262144 bf16 183 us.  One row of 151936 takes 4.7 us without and 7.6 with 20 alternatives:
 // a cluster of 16 CTAs, two cluster barriers, the choice of tiles and the candidates between them.
 // After a flush of L2, on 1088 x 151936 fp32 unless stated, while this was built: CTAs of 8 warps, four to
-// an SM, hide each other's row ends better than two of 16 (131 against 141 us); a ring filled by 16-byte
-// asynchronous copies measured 139 us (its shared-memory traffic competes with the exponentials), two or
-// three tiles ahead 133 and 143 (fewer warps fit), and values clamped one by one against -inf in every
-// tile 204 us at 2048 x 262144 bf16 (hence the two forms of the loop).
+// an SM, hide each other's row ends better than two of 16 (131 against 141 us; five with 48 registers,
+// among other calls, 116 against 102); a ring filled by 16-byte asynchronous copies measured 139 us (its
+// shared-memory traffic competes with the exponentials), two or three tiles ahead 133 and 143 (fewer warps
+// fit), and values clamped one by one against -inf in every tile 204 us at 2048 x 262144 bf16 (hence the
+// two forms of the loop).
 //
 // Alternatives.  The main pass spends nothing on them beyond the tiles' maxima.  The k best elements
 // (value descending, index ascending) lie in the k best tiles ordered by (maximum descending, tile
@@ -251,7 +252,7 @@ template <int DT, bool CLUSTER>
 struct WarpSums {
   using E = Elem<DT>;
   static constexpr int kPairs = E::kVec / 2, kLoads = RowTiles<DT>::kLoads;
-  static constexpr int kAhead = 1;  // (two in 16 bits: 213 against 188 us for 2048 x 262144 bf16, registers spill)
+  static constexpr int kAhead = 1;  // (two in 16 bits: 208 against 183 us for 2048 x 262144 bf16, registers spill)
   float c, R;
   float2 S2, E2;
   bool clamp;
