@@ -256,29 +256,38 @@ __global__ void __launch_bounds__(kMqThreads, 1)
       // both scales before the wait: lane i holds the tokens' i, i + 32, ...
       const float sw = mine ? a.w_scale[v] : 0.f;
       float sq[kMqMaxTokens / 32];
+      static_assert(kMqMaxTokens == 128, "four scales a lane");
 #pragma unroll
       for (int i = 0; i < kMqMaxTokens / 32; ++i) sq[i] = i * 32 + lane < nm ? a.q_scale[m0 + i * 32 + lane] : 0.f;
       const bool ok = __all_sync(0xffffffffu, mq_wait(sy, &t_full[buf], acc_r.phase));
       tc_fence_after();
       if (b < a.blocks) {
         const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)((buf * a.blocks + b) * a.bn);
-#pragma unroll
-        for (int i = 0; i < kMqMaxTokens / 16; ++i) {
-          const int c = i * 16;
-          if (c >= nm) break;
-          if ((i & 1) != h) continue;
+#pragma unroll 1
+        for (int c = h * 16; c < nm; c += 32) {
+          const float sc = c < 32 ? sq[0] : c < 64 ? sq[1] : c < 96 ? sq[2] : sq[3];
           uint32_t r[16];
           if (ok) {
             tmem_ld_x16(acc + c, r);
             tmem_wait_ld();
           }
-          long long o = (long long)(m0 + c) * a.ldo + v;
+          // all values before the first store: one branch a value cost 0.8 us a chunk
+          float o[16];
 #pragma unroll
-          for (int j = 0; j < 16; ++j, o += a.ldo) {
-            const float s = __shfl_sync(0xffffffffu, sq[i / 2], (c + j) & 31);
-            if (c + j < nm && mine)
-              store_out<DT>(a.out, o, ok ? (float)(int32_t)r[j] * s * sw : __int_as_float(0x7FC00000));
+          for (int j = 0; j < 16; ++j) {
+            const float s = __shfl_sync(0xffffffffu, sc, (c + j) & 31);
+            o[j] = ok ? (float)(int32_t)r[j] * s * sw : __int_as_float(0x7FC00000);
           }
+          long long at = (long long)(m0 + c) * a.ldo + v;
+          if (mine && c + 16 <= nm) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j, at += a.ldo) store_out<DT>(a.out, at, o[j]);
+          } else if (mine) {
+#pragma unroll
+            for (int j = 0; j < 15; ++j, at += a.ldo)
+              if (c + j < nm) store_out<DT>(a.out, at, o[j]);
+          }
+          __syncwarp();
         }
         if (!ok && a.flags && q == 0 && b == 0 && h == 0)
           for (int m = m0 + lane; m < m0 + nm; m += 32) atomicOr(a.flags + m, DSPARK_FLAG_DEVICE_TIMEOUT);
