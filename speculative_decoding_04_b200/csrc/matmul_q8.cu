@@ -35,9 +35,10 @@ constexpr int kMqKB = 128;    // bytes (= values) of a block of K: one swizzled 
 constexpr int kMqBlocks = 2;  // blocks of K per stage
 constexpr int kMqMaxStages = 8;
 constexpr uint32_t kMqSmem = 227u * 1024u;
-// Tokens of one single-CTA call; more than this: CTA pairs.  (151936 x 4096, fp32 out, one CTA a tile
-// against pairs: 40 tokens 117 and 123 us, 80 121 and 125, 100 127 and 127, 128 131 and 129.)
-constexpr int kMqMaxTokens = 128;
+// Tokens of one single-CTA call; more than this: CTA pairs.  (One CTA a tile against pairs: 151936 x 4096,
+// fp32 out, 40 tokens 101 and 107 us, 80 108 and 113, 84 116 and 112, 100 124 and 117, 128 131 and 122;
+// 129280 x 2048, bf16 out, 64 48 and 49, 84 57 and 50, 128 59 and 55.)
+constexpr int kMqMaxTokens = 80;
 
 struct MqArgs {
   const float* q_scale;
@@ -48,7 +49,7 @@ struct MqArgs {
   int M, N, K;
   int bv, bn;          // tile: weight rows (multiple of 16, <= 256), tokens (multiple of 16, <= 256)
   int ntok, ntiles;    // token tiles; tiles in all
-  int stages, nbuf, blocks, tmem_cols;
+  int stages, blocks, tmem_cols;
   uint32_t w_bytes, x_bytes;            // one block of K: bytes of the tile's weights and tokens
   uint32_t x_off, stage_bytes, bars;    // tokens within a stage; a stage; barriers after the stages
   uint32_t out_off;                     // (CTA pairs) staging of the output
@@ -215,7 +216,7 @@ __global__ void __launch_bounds__(kMqThreads, 1)
       MqRing r{0, 0}, acc_r{0, 0};
       const uint64_t desc0 = smem_desc(smem_u32(sm), 16u, 1024u, 2u);  // + bytes / 16 for any stage and block
       bool ok = true;
-      for (int t = blockIdx.x; ok && t < a.ntiles; t += gridDim.x, acc_r.next(a.nbuf)) {
+      for (int t = blockIdx.x; ok && t < a.ntiles; t += gridDim.x, acc_r.next(2)) {
         const int buf = acc_r.s;
         if (!mq_wait(sy, &t_empty[buf], acc_r.phase ^ 1u)) break;
         tc_fence_after();
@@ -245,27 +246,27 @@ __global__ void __launch_bounds__(kMqThreads, 1)
     }
   } else if (warp >= 4) {
     // lane quadrant, block of 128 weight rows, and which of the alternating chunks of 16 tokens: the last
-    // tile's epilogue runs alone (128 x 50000 x 1024: 25 us, 29 with half as many warps)
+    // tile's epilogue runs alone (128 x 50000 x 1024 took 29 us with half as many warps and 25 with these)
     const int q = warp & 3, b = ((warp - 4) >> 2) & 1, h = (warp - 4) >> 3;
     MqRing acc_r{0, 0};
-    for (int t = blockIdx.x; t < a.ntiles; t += gridDim.x, acc_r.next(a.nbuf)) {
+    for (int t = blockIdx.x; t < a.ntiles; t += gridDim.x, acc_r.next(2)) {
       const int buf = acc_r.s;
       const int v = (t / a.ntok) * a.bv + b * 128 + q * 32 + lane, m0 = (t % a.ntok) * a.bn;
       const bool mine = b < a.blocks && b * 128 + q * 32 + lane < a.bv && v < a.N;
       const int nm = min(a.bn, a.M - m0);
       // both scales before the wait: lane i holds the tokens' i, i + 32, ...
       const float sw = mine ? a.w_scale[v] : 0.f;
-      float sq[kMqMaxTokens / 32];
-      static_assert(kMqMaxTokens == 128, "four scales a lane");
+      float sq[3];
+      static_assert(kMqMaxTokens <= 3 * 32, "three scales a lane");
 #pragma unroll
-      for (int i = 0; i < kMqMaxTokens / 32; ++i) sq[i] = i * 32 + lane < nm ? a.q_scale[m0 + i * 32 + lane] : 0.f;
+      for (int i = 0; i < 3; ++i) sq[i] = i * 32 + lane < nm ? a.q_scale[m0 + i * 32 + lane] : 0.f;
       const bool ok = __all_sync(0xffffffffu, mq_wait(sy, &t_full[buf], acc_r.phase));
       tc_fence_after();
       if (b < a.blocks) {
         const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)((buf * a.blocks + b) * a.bn);
 #pragma unroll 1
         for (int c = h * 16; c < nm; c += 32) {
-          const float sc = c < 32 ? sq[0] : c < 64 ? sq[1] : c < 96 ? sq[2] : sq[3];
+          const float sc = c < 32 ? sq[0] : c < 64 ? sq[1] : sq[2];
           uint32_t r[16];
           if (ok) {
             tmem_ld_x16(acc + c, r);
@@ -693,9 +694,8 @@ dspark_status launch_matmul_q8(const MatmulQ8Call& c) {
     a.bv = (int)std::min(256ll, std::max(16ll, (rows + 15) / 16 * 16));
     a.ntiles = a.ntok * ((c.N + a.bv - 1) / a.bv);
     a.blocks = a.bv > 128 ? 2 : 1;
-    a.nbuf = 2 * a.blocks * a.bn <= 512 ? 2 : 1;
     a.tmem_cols = 32;
-    while (a.tmem_cols < a.nbuf * a.blocks * a.bn) a.tmem_cols *= 2;
+    while (a.tmem_cols < 2 * a.blocks * a.bn) a.tmem_cols *= 2;
     a.w_bytes = (uint32_t)(a.bv * kMqKB);
     a.x_bytes = (uint32_t)(a.bn * kMqKB);
     a.x_off = kMqBlocks * a.w_bytes;

@@ -135,6 +135,16 @@ def test_matmul_sizes(M, N, K):
         assert torch.equal(D.matmul_q8(q, qs, w, ws, out_dtype=DT[dtype]), out)
 
 
+@pytest.mark.parametrize("M", [79, 80, 81, 95, 96, 97, 112])
+def test_matmul_sizes_about_the_change_of_form(M):
+    rng = np.random.default_rng(M)
+    for N, K in ((2000, 128), (40003, 300)):
+        q, w = make_q(rng, M, K), make_q(rng, N, K)
+        qs, ws = torch.rand(M, device="cuda"), torch.rand(N, device="cuda")
+        for dtype in ("f32", "bf16"):
+            check_matmul(q, qs, w, ws, D.matmul_q8(q, qs, w, ws, out_dtype=DT[dtype]), dtype)
+
+
 def test_matmul_extremes():
     """The largest sums int32 holds: K = 131071 of -128 * -128, and alternating signs."""
     K = 131071
