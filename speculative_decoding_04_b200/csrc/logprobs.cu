@@ -331,7 +331,18 @@ struct WarpSums {
       }
       clamp = true;
     }
-    if (R == -INFINITY && m == -INFINITY) return;  // nothing unmasked so far
+    if (R == -INFINITY && m == -INFINITY) {  // nothing unmasked so far: -inf adds nothing, NaN stays
+      float x = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < kLoads; ++j)
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i) {
+          const float2 p = E::pair(v[j], i);
+          x = max3_nan(x, p.x, p.y);
+        }
+      if (x != x) S2.x = x;  // (the maxima m and R are taken past NaN)
+      return;
+    }
     float2 ts, te;
 #pragma unroll
     for (int j = 0; j < kLoads; ++j)
