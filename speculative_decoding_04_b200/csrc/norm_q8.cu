@@ -142,14 +142,18 @@ __device__ __forceinline__ float2 row_scale(const NqArgs& a, float ss, float A, 
   if (A < 0x1p-120f) return make_float2(0.f, 0.f);
   const float f = __fdiv_rn(127.f, A);
   if (!a.norm) return make_float2(__fdiv_rn(A, 127.f), f);
-  // ss holds the squares of h * ss_unit (a power of two, 1 unless the squares overflow)
-  const float inv = __frsqrt_rn(ss / (float)a.d + a.eps * ss_unit * ss_unit) * ss_unit;
-  return make_float2(__fmul_rn(__fmul_rn(A, inv), 1.f / 127.f), f);
+  // ss holds the squares of h * ss_unit (a power of two, 1 unless the squares overflow).  The unit goes to
+  // the larger factor: 2^-128, the inverse for the largest rows, is a denormal.
+  const float inv = __frsqrt_rn(ss / (float)a.d + a.eps * ss_unit * ss_unit);
+  const float y = A > 1.f ? __fmul_rn(__fmul_rn(A, ss_unit), inv) : __fmul_rn(A, __fmul_rn(inv, ss_unit));
+  return make_float2(__fmul_rn(y, 1.f / 127.f), f);
 }
 
 __device__ __forceinline__ int8_t to_q8(float v, float f) { return (int8_t)__float2int_rn(__fmul_rn(v, f)); }
 
-constexpr float kTiny = 0x1p-70f;
+// The unit of rows whose squares overflow.  Such a row holds |h| >= 2^48 (d < 2^31): (2^48 kTiny)^2 is 2^-84,
+// and the squares of 2^31 values below 2^128 sum to less than 2^107.
+constexpr float kTiny = 0x1p-90f;
 
 // Two products v f (each rounded) to the nearest integers, ties to even: adding 1.5 * 2^23 leaves the
 // integer in the low bits of the sum.  (Scalar instructions: a packed product followed by a packed
