@@ -457,7 +457,8 @@ int dspark_token_logprobs(const void* logits, int dtype, int64_t ld, int64_t n_r
  * g_logp    [N] fp32 or NULL (0).  g_entropy [N] fp32 or NULL (0).
  * top_idx   [N, top] int32 and g_top [N, top] fp32, required when top > 0.
  * grad      [N, V] of the logits' dtype, rows ldg elements apart.  It may be the logits themselves
- *           (same address and ldg == ld); any other overlap is refused.
+ *           (same address and ldg == ld); any other overlap is refused (columns of one buffer side by
+ *           side do not overlap; of arrays with different strides the address ranges decide).
  * Other arguments as dspark_token_logprobs.  No workspace.
  * -------------------------------------------------------------------------- */
 int dspark_token_logprobs_backward(const void* logits, int dtype, int64_t ld, const int32_t* tokens, int N, int V,
@@ -483,7 +484,8 @@ int dspark_token_logprobs_backward(const void* logits, int dtype, int64_t ld, co
  * gain      [d] of gain_dtype (dtype itself or DSPARK_F32), or NULL (1).
  * eps       >= 2^-100, finite.
  * h_out     [M, d] of dtype, rows ldh apart: required with a residual, ignored without.  It may be x
- *           or the residual itself (same address and stride).
+ *           or the residual itself (same address and stride); any other overlap is refused, as for the
+ *           gradient of dspark_token_logprobs_backward.
  * q         [M, d] int8, rows ldq bytes apart (a multiple of 16 for dspark_matmul_q8).
  * scale     [M] fp32.
  * q and scale overlap no input.  M = 0 does nothing.  No workspace.

@@ -87,11 +87,16 @@ static size_t dtype_bytes(int dtype) {
   return dtype == DSPARK_F32 ? 4 : dtype == DSPARK_BF16 || dtype == DSPARK_F16 ? 2 : 0;
 }
 
-// Two [rows, cols] arrays with element size es share memory without being the same array.
+// Two [rows, cols] arrays with element size es share memory without being the same array.  Arrays of one
+// stride may lie between each other's rows (columns of one buffer); of others the address ranges decide.
 static bool bad_overlap(const void* a, int64_t lda, const void* b, int64_t ldb, int rows, int cols, size_t es) {
-  const char *a0 = static_cast<const char*>(a), *b0 = static_cast<const char*>(b);
-  const char *a1 = a0 + ((size_t)(rows - 1) * lda + cols) * es, *b1 = b0 + ((size_t)(rows - 1) * ldb + cols) * es;
-  return a0 < b1 && b0 < a1 && !(a0 == b0 && (lda == ldb || rows == 1));
+  if (a == b && (lda == ldb || rows == 1)) return false;
+  const uintptr_t a0 = (uintptr_t)a, b0 = (uintptr_t)b;
+  const uintptr_t row = cols * es, a1 = a0 + (size_t)(rows - 1) * lda * es + row, b1 = b0 + (size_t)(rows - 1) * ldb * es + row;
+  if (a0 >= b1 || b0 >= a1) return false;
+  if (lda != ldb || rows == 1) return true;
+  const uintptr_t step = lda * es, off = (a0 > b0 ? a0 - b0 : b0 - a0) % step;
+  return off < row || off > step - row;
 }
 
 static dspark_status einval(const std::string& msg) {
