@@ -172,8 +172,12 @@ Tensor token_logprobs_backward(const Tensor& logits, const Tensor& tokens, doubl
     grad = *grad_;
     g = like(grad, "grad", logits, logits.scalar_type());
   } else {
-    grad = at::detail::empty_strided_cuda({l.rows, l.cols}, {l.ld, 1}, logits.scalar_type(), logits.device());
-    g = Rows{static_cast<char*>(grad.data_ptr()), l.rows, l.cols, l.ld};
+    // Rows as far apart as the logits', so that both start at the same offset within 16 bytes; where a lot
+    // lies between the logits' rows (one position of each request), the nearest such distance.
+    const int64_t vec = 16 / logits.element_size(), most = l.cols + std::max<int64_t>(l.cols, 1024);
+    const int64_t ldg = l.ld <= most ? l.ld : l.cols + (l.ld - l.cols) % vec;
+    grad = at::detail::empty_strided_cuda({l.rows, l.cols}, {ldg, 1}, logits.scalar_type(), logits.device());
+    g = Rows{static_cast<char*>(grad.data_ptr()), l.rows, l.cols, ldg};
     if (logits.dim() != 2) grad = grad.view(logits.sizes());
   }
   check("dspark_token_logprobs_backward",

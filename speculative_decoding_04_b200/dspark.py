@@ -516,8 +516,8 @@ def token_logprobs_backward(logits: torch.Tensor, tokens: torch.Tensor, T: float
 
     stats, entropy: what the forward call returned; g_logp, g_entropy and g_top ([..., top], with the
     forward's top_idx): the gradients of its outputs, each or None.  grad: where to write it -- the
-    logits' dtype and shape, the logits themselves among them -- or None: a new tensor with the strides
-    of the logits' rows."""
+    logits' dtype and shape, the logits themselves among them -- or None: a new tensor whose rows are as
+    far apart as the logits' (or nearly dense, where more than a row's length lies between those)."""
     return _call(_binding.token_logprobs_backward, stream, logits, tokens, T, stats, entropy, g_logp, g_entropy, top_idx,
                  g_top, grad)
 
