@@ -3,7 +3,8 @@
     python -m speculative_decoding_04_b200.build [--verbose]
 
 The library is written to speculative_decoding_04_b200/lib/libdspark.so, the binding (csrc/binding.cpp)
-beside it as the extension module lib/_binding.
+beside it as an extension module with torch's version in its name: one built against another torch is
+never loaded.
 """
 import glob
 import os
@@ -16,7 +17,6 @@ ROOT = os.path.dirname(HERE)
 LIB_DIR = os.path.join(HERE, "lib")
 LIB_PATH = os.path.join(LIB_DIR, "libdspark.so")
 BINDING_SRC = os.path.join(HERE, "csrc", "binding.cpp")
-BINDING_PATH = os.path.join(LIB_DIR, "_binding" + sysconfig.get_config_var("EXT_SUFFIX"))
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -57,10 +57,18 @@ def run(cmd, what, verbose):
         raise RuntimeError(f"{cmd[0]} failed building {what}")
 
 
+def binding_path():
+    import torch
+
+    tag = "".join(c if c.isalnum() else "_" for c in torch.__version__)
+    return os.path.join(LIB_DIR, f"_binding_torch{tag}" + sysconfig.get_config_var("EXT_SUFFIX"))
+
+
 def needs_binding():
-    if not os.path.exists(BINDING_PATH):
+    path = binding_path()
+    if not os.path.exists(path):
         return True
-    t = os.path.getmtime(BINDING_PATH)
+    t = os.path.getmtime(path)
     return any(os.path.getmtime(d) > t for d in [BINDING_SRC] + glob.glob(os.path.join(ROOT, "include", "*.h")))
 
 
@@ -71,7 +79,8 @@ def build_binding(verbose=False):
     cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
     inc = [os.path.join(torch_dir, "include"), os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
            os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
-    tmp = BINDING_PATH + ".tmp"
+    path = binding_path()
+    tmp = path + ".tmp"
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-DTORCH_EXTENSION_NAME=_binding",
            "-DTORCH_API_INCLUDE_EXTENSION_H", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
     cmd += ["-isystem" + d for d in inc] + [BINDING_SRC, "-o", tmp, "-L" + LIB_DIR, "-l:libdspark.so",
@@ -79,7 +88,7 @@ def build_binding(verbose=False):
                                             "-ltorch_cpu", "-ltorch_cuda", "-ltorch", "-ltorch_python",
                                             "-Wl,-rpath,$ORIGIN"]
     run(cmd, "the torch binding", verbose)
-    os.replace(tmp, BINDING_PATH)
+    os.replace(tmp, path)
 
 
 def build(verbose=False, force=False, ptxas_verbose=False):

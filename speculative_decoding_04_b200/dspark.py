@@ -5,7 +5,8 @@ Every function takes CUDA torch tensors, checks dtype / shape / contiguity,
 passes raw device pointers and the current CUDA stream to the C ABI declared
 in include/dspark.h, and raises DsparkError on a non-zero status.  All
 arithmetic runs in the library's CUDA kernels; there is no CPU fallback:
-importing this module raises if the library has not been built.
+importing this module raises if the library has not been built, and the
+first call that needs the extension module if that is missing.
 """
 
 from __future__ import annotations
@@ -19,7 +20,7 @@ from typing import Optional, Tuple
 import numpy as np
 import torch
 
-from .build import BINDING_PATH, LIB_PATH, ROOT
+from .build import LIB_PATH, ROOT, binding_path
 
 OK, EINVAL, ECUDA, ENOTIMPL, ETIMEOUT = 0, 1, 2, 3, 4
 F32, BF16, F16 = 0, 1, 2
@@ -113,17 +114,21 @@ def _load() -> ctypes.CDLL:
 lib = _load()
 
 
-def _load_binding():
-    # the extension module of the LM-head and log-probability entry points (csrc/binding.cpp)
-    if not os.path.exists(BINDING_PATH):
-        raise ImportError(f"{BINDING_PATH} is missing: build it with `python -m speculative_decoding_04_b200.build`")
-    spec = importlib.util.spec_from_file_location("_binding", BINDING_PATH)
-    mod = importlib.util.module_from_spec(spec)
-    spec.loader.exec_module(mod)
-    return mod
+class _Binding:
+    # the extension module of the LM-head and log-probability entry points (csrc/binding.cpp), loaded by
+    # the first of their calls: the others need ctypes alone
+    def __getattr__(self, name):
+        path = binding_path()
+        if not os.path.exists(path):
+            raise ImportError(f"{path} is missing: build it with `python -m speculative_decoding_04_b200.build`")
+        spec = importlib.util.spec_from_file_location("_binding", path)
+        mod = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(mod)
+        self.__dict__.update((k, v) for k, v in vars(mod).items() if not k.startswith("_"))
+        return object.__getattribute__(self, name)
 
 
-_binding = _load_binding()
+_binding = _Binding()
 
 
 def declared_functions() -> list:
