@@ -111,7 +111,8 @@ const char* dspark_last_error(void);
  *                     device waits (draft and 8-bit product: polls per wait; streaming verify:
  *                     nanoseconds; 0: the defaults of about a second and 2 s); the second makes one wait unsatisfiable
  *                     (1: the fused draft's first grid barrier, 2: the streaming verify's cluster
- *                     exchange, 3: the 8-bit product's accumulators), so that a test can check that the kernel returns with
+ *                     exchange, 3: the 8-bit product's accumulators, 4: the same for one warp of each
+ *                     CTA alone), so that a test can check that the kernel returns with
  *                     DSPARK_ETIMEOUT in the workspace status and DEVICE_TIMEOUT in the flags
  *                     (the 8-bit product has no workspace: flags, and NaN in the outputs)
  * The environment variables DSPARK_DRAFT_TC_MIN_B, DSPARK_DRAFT_PATH, DSPARK_DRAFT_PDL,

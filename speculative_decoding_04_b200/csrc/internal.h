@@ -28,7 +28,9 @@ struct Options {
   // test-only: make the bounded device waits give up sooner and one of them unsatisfiable, so that
   // a test can check that the kernels return with a timeout status (never on in normal use)
   long debug_wait_limit = 0;      // draft, 8-bit product: polls per wait; streaming verify: nanoseconds (0: defaults)
-  int debug_unreachable_barrier = 0;  // 1: the draft's first grid barrier; 2: the streaming verify's exchange; 3: the 8-bit product's accumulators
+  // 1: the draft's first grid barrier; 2: the streaming verify's exchange; 3: the 8-bit product's
+  // accumulators; 4: the same, for one of a CTA's warps
+  int debug_unreachable_barrier = 0;
 };
 // A copy of the process-wide options, taken under their lock (dspark_set_option may run on
 // another thread).

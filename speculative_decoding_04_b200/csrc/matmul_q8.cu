@@ -56,6 +56,7 @@ struct MqArgs {
   int out_tma;                          // (CTA pairs) the output takes TMA stores
   uint32_t spin_limit;                  // polls before a bounded wait gives up
   int barrier_extra;                    // test-only: arrivals the accumulators' barriers expect beyond the commit
+  int lost_warp;                        // test-only: an epilogue warp whose waits count as given up, or -1
 };
 
 // Tensor maps of the weights and the tokens: [rows, K] with boxes of 128 bytes of K by the tile's rows,
@@ -260,7 +261,7 @@ __global__ void __launch_bounds__(kMqThreads, 1)
       static_assert(kMqMaxTokens <= 3 * 32, "three scales a lane");
 #pragma unroll
       for (int i = 0; i < 3; ++i) sq[i] = i * 32 + lane < nm ? a.q_scale[m0 + i * 32 + lane] : 0.f;
-      const bool ok = __all_sync(0xffffffffu, mq_wait(sy, &t_full[buf], acc_r.phase));
+      const bool ok = __all_sync(0xffffffffu, mq_wait(sy, &t_full[buf], acc_r.phase)) && warp != a.lost_warp;
       tc_fence_after();
       if (b < a.blocks) {
         const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)((buf * a.blocks + b) * a.bn);
@@ -290,8 +291,10 @@ __global__ void __launch_bounds__(kMqThreads, 1)
           }
           __syncwarp();
         }
-        if (!ok && a.flags && q == 0 && b == 0 && h == 0)
-          for (int m = m0 + lane; m < m0 + nm; m += 32) atomicOr(a.flags + m, DSPARK_FLAG_DEVICE_TIMEOUT);
+        if (!ok && a.flags && __any_sync(0xffffffffu, mine)) {  // each warp for the tokens it wrote as NaN
+          for (int c = h * 16 + lane; lane < 16 && c < nm; c += 32) atomicOr(a.flags + m0 + c, DSPARK_FLAG_DEVICE_TIMEOUT);
+          __syncwarp();
+        }
       }
       tc_fence_before();
       __syncwarp();
@@ -315,6 +318,7 @@ __global__ void __launch_bounds__(kMqThreads, 1)
 constexpr int kPairGroups = 4;  // of four epilogue warps
 constexpr int kPairEpiWarps = 4 * kPairGroups;
 constexpr int kPairThreads = 128 + 32 * kPairEpiWarps;
+static_assert(kPairThreads == kMqThreads, "the last warp of either form");
 constexpr int kPairMaxStages = 8;
 constexpr int kOutTokens = 16;  // tokens of one staged store
 
@@ -508,7 +512,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         return c + lane < nm && lane < kOutTokens ? a.q_scale[m0 + c + lane] : 0.f;
       };
       float sq = scale_of(h * kOutTokens);
-      const bool ok = __all_sync(0xffffffffu, mq_wait(sy, &t_full[buf], acc_r.phase));
+      const bool ok = __all_sync(0xffffffffu, mq_wait(sy, &t_full[buf], acc_r.phase)) && warp != a.lost_warp;
       tc_fence_after();
       const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * a.bn);
       uint32_t r[16];
@@ -567,8 +571,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           }
         }
       }
-      if (!ok && a.flags && q == 0 && h == 0)
-        for (int m = m0 + lane; m < m0 + nm; m += 32) atomicOr(a.flags + m, DSPARK_FLAG_DEVICE_TIMEOUT);
+      if (!ok && a.flags && v0 + q * 32 < a.N)  // each warp for the tokens it wrote as NaN
+        for (int c = h * kOutTokens + lane; lane < kOutTokens && c < nm; c += kPairGroups * kOutTokens)
+          atomicOr(a.flags + m0 + c, DSPARK_FLAG_DEVICE_TIMEOUT);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(mapa_rank(smem_u32(&t_empty[buf]), 0));
@@ -659,6 +664,7 @@ dspark_status launch_matmul_q8(const MatmulQ8Call& c) {
   const Options opt = options();
   a.spin_limit = opt.debug_wait_limit > 0 ? (uint32_t)opt.debug_wait_limit : kSpinLimit;
   a.barrier_extra = opt.debug_unreachable_barrier == 3 ? 1 : 0;
+  a.lost_warp = opt.debug_unreachable_barrier == 4 ? kMqThreads / 32 - 1 : -1;
   a.M = c.M;
   a.N = c.N;
   a.K = c.K;
