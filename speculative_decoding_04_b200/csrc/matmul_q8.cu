@@ -249,6 +249,10 @@ __global__ void __launch_bounds__(kMqThreads, 1)
     // lane quadrant, block of 128 weight rows, and which of the alternating chunks of 16 tokens: the last
     // tile's epilogue runs alone (128 x 50000 x 1024 took 29 us with half as many warps and 25 with these)
     const int q = warp & 3, b = ((warp - 4) >> 2) & 1, h = (warp - 4) >> 3;
+    // A warp whose wait gave up is done with the barriers: a parity does not tell a phase from the one two
+    // later, and an arrival more would hand an accumulator on that other warps still read.  It writes NaN
+    // from there on; the issuer, without its arrivals, gives up too.
+    bool ok = warp != a.lost_warp;
     MqRing acc_r{0, 0};
     for (int t = blockIdx.x; t < a.ntiles; t += gridDim.x, acc_r.next(2)) {
       const int buf = acc_r.s;
@@ -261,7 +265,7 @@ __global__ void __launch_bounds__(kMqThreads, 1)
       static_assert(kMqMaxTokens <= 3 * 32, "three scales a lane");
 #pragma unroll
       for (int i = 0; i < 3; ++i) sq[i] = i * 32 + lane < nm ? a.q_scale[m0 + i * 32 + lane] : 0.f;
-      const bool ok = __all_sync(0xffffffffu, mq_wait(sy, &t_full[buf], acc_r.phase)) && warp != a.lost_warp;
+      ok = __all_sync(0xffffffffu, ok && mq_wait(sy, &t_full[buf], acc_r.phase));
       tc_fence_after();
       if (b < a.blocks) {
         const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)((buf * a.blocks + b) * a.bn);
@@ -298,7 +302,7 @@ __global__ void __launch_bounds__(kMqThreads, 1)
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&t_empty[buf]);
+      if (ok && lane == 0) mbar_arrive(&t_empty[buf]);
     }
   }
   tc_fence_before();
@@ -502,6 +506,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     const int q = warp & 3, h = (warp - 4) >> 2, gt = q * 32 + lane;
     const bool issuer = q == 0 && lane == 0;
     uint8_t* stage = sm + a.out_off + (uint32_t)h * (kOutTokens * (a.out_tma ? 128u * kEs : kPitch));
+    bool ok = warp != a.lost_warp;  // (as in the form of one CTA)
     MqRing acc_r{0, 0};
     for (int t = pair; t < a.ntiles; t += npairs, acc_r.next(2)) {
       const int buf = acc_r.s;
@@ -512,7 +517,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         return c + lane < nm && lane < kOutTokens ? a.q_scale[m0 + c + lane] : 0.f;
       };
       float sq = scale_of(h * kOutTokens);
-      const bool ok = __all_sync(0xffffffffu, mq_wait(sy, &t_full[buf], acc_r.phase)) && warp != a.lost_warp;
+      ok = __all_sync(0xffffffffu, ok && mq_wait(sy, &t_full[buf], acc_r.phase));
       tc_fence_after();
       const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * a.bn);
       uint32_t r[16];
@@ -576,7 +581,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           atomicOr(a.flags + m0 + c, DSPARK_FLAG_DEVICE_TIMEOUT);
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(mapa_rank(smem_u32(&t_empty[buf]), 0));
+      if (ok && lane == 0) mbar_arrive_cluster(mapa_rank(smem_u32(&t_empty[buf]), 0));
     }
     if (issuer) bulk_wait0();
   }

@@ -57,3 +57,24 @@ def test_one_warp_gives_up(M, N, dtype):
     tile = M if M <= 80 else (M // (1 + (M > 256)) + 31) // 32 * 32
     rows = (np.arange(M) % tile) % step >= step - 16
     assert np.array_equal(lost.any(-1), rows) and 0 < lost[rows].mean() < 0.5
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("M,N", [(40, 150000), (7, 100001), (300, 60001), (600, 40000)])
+def test_waits_give_up_in_calls_of_many_tiles(M, N, dtype):
+    """More than two tiles a CTA: an accumulator's barrier is used again, and a parity waited for in vain at
+    one tile is met at once two tiles on."""
+    a = problem(M, N)
+    out, flags = with_option(3, a, dtype)
+    assert check_partial(a, out, flags, dtype).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("M,N", [(40, 150000), (300, 60001)])
+def test_one_warp_gives_up_in_calls_of_many_tiles(M, N, dtype):
+    """Without that warp's arrivals the third tile's products are not issued: its outputs are lost, the first
+    two tiles' are right but for the warp's own."""
+    a = problem(M, N)
+    out, flags = with_option(4, a, dtype)
+    lost = check_partial(a, out, flags, dtype)
+    assert lost.any(-1).all() and 0 < lost.mean() < 1
