@@ -451,11 +451,15 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         }
       }
       // rank 0 lets the copies of both CTAs land (bounded), whoever was to wait for them; rank 1 waits for
-      // it at the last cluster barrier
-      if (rank == 0)
+      // it at the last cluster barrier.  Where rank 1 gave up it may have issued copies that rank 0 does
+      // not count: they land within microseconds
+      if (rank == 0) {
         for (int i = max(0, it - a.stages); i < it; ++i)
           for (uint32_t n = 0; n < kSpinLimit && !mbar_try_wait(&full[i % a.stages], (i / a.stages) & 1); ++n) {
           }
+      } else if (!ok) {
+        __nanosleep(1000000);
+      }
     }
   } else if (warp == 1) {
     if (rank == 0 && lane == 0) {
@@ -491,6 +495,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       }
       tc_commit_pair(drain);  // tensor memory and the stages stay until the MMAs already issued are done (bounded)
       mbar_wait(drain, 0);
+    } else if (lane == 0) {
+      mbar_wait(drain, 0);  // the last of rank 0's arrivals at this CTA's barriers (bounded)
     }
   } else if (warp >= 4) {
     // The four warps of a group h hold 128 consecutive outputs of a token on their lanes.  Chunks of 16
