@@ -673,7 +673,7 @@ dspark_status launch_matmul_q8(const MatmulQ8Call& c) {
   a.ldo = c.ldo;
   a.flags = c.flags;
   const Options opt = options();
-  a.spin_limit = opt.debug_wait_limit > 0 ? (uint32_t)opt.debug_wait_limit : kSpinLimit;
+  a.spin_limit = opt.debug_wait_limit > 0 ? (uint32_t)std::min<long>(opt.debug_wait_limit, kSpinLimit) : kSpinLimit;
   a.barrier_extra = opt.debug_unreachable_barrier == 3 ? 1 : 0;
   a.lost_warp = opt.debug_unreachable_barrier == 4 ? kMqThreads / 32 - 1 : -1;
   a.M = c.M;

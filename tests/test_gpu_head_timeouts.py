@@ -78,3 +78,18 @@ def test_one_warp_gives_up_in_calls_of_many_tiles(M, N, dtype):
     out, flags = with_option(4, a, dtype)
     lost = check_partial(a, out, flags, dtype)
     assert lost.any(-1).all() and 0 < lost.mean() < 1
+
+
+@pytest.mark.parametrize("M", [3, 100])
+@pytest.mark.parametrize("limit", [1 << 32, (1 << 33) + 1, 1 << 40])
+def test_a_long_limit_is_not_cut_to_a_short_one(M, limit):
+    a = problem(M, 5000, 2000)
+    flags = torch.zeros(M, dtype=torch.int32, device="cuda")
+    D.set_option("debug_wait_limit", limit)
+    try:
+        out = D.matmul_q8(*a, flags=flags)
+        torch.cuda.synchronize()
+    finally:
+        D.set_option("debug_wait_limit", 0)
+    assert not host(flags).any()
+    check_matmul(*a, out, "f32")
