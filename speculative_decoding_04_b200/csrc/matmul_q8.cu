@@ -123,7 +123,15 @@ __device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&r)[16]) {
       : "r"(taddr)
       : "memory");
 }
-__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// Waits for the loads issued so far.  It names the registers of the load, so that nothing uses or copies
+// them between the two.
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
 
 template <int DT>
 __device__ __forceinline__ void store_out(void* out, long long i, float v) {
@@ -275,7 +283,7 @@ __global__ void __launch_bounds__(kMqThreads, 1)
           uint32_t r[16];
           if (ok) {
             tmem_ld_x16(acc + c, r);
-            tmem_wait_ld();
+            tmem_wait_ld(r);
           }
           // all values before the first store: one branch a value cost 0.8 us a chunk
           float o[16];
@@ -529,7 +537,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       uint32_t r[16];
       if (ok && h * kOutTokens < nm) tmem_ld_x16(acc + h * kOutTokens, r);
       for (int c = h * kOutTokens; c < nm; c += kPairGroups * kOutTokens) {
-        if (ok) tmem_wait_ld();
+        if (ok) tmem_wait_ld(r);
         float o[16];
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
