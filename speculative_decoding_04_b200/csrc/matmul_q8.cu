@@ -707,7 +707,9 @@ dspark_status launch_matmul_q8(const MatmulQ8Call& c) {
     a.stages = (int)std::min<uint32_t>(kPairMaxStages, (kMqSmem - 1024 - misc - staging) / a.stage_bytes);
     a.out_off = a.stages * a.stage_bytes;
     a.bars = a.out_off + staging;
-    a.out_tma = (uintptr_t)c.out % 16 == 0 && c.ldo * es % 16 == 0 && c.ldo * es < (1ll << 40);
+    // (rows that end within 16 bytes too: a TMA store writes the whole of the 16 bytes that N ends in, over
+    // what lies beside the output)
+    a.out_tma = (uintptr_t)c.out % 16 == 0 && c.ldo * es % 16 == 0 && (long long)c.N * es % 16 == 0 && c.ldo * es < (1ll << 40);
     box_v = 128;
     box_m = a.bn / 2;
     grid = 2 * std::min(std::max(1, sms / 2), a.ntiles);
