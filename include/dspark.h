@@ -437,7 +437,8 @@ int dspark_prefix_schedule_t2(const float* c, const double* sps, int B, int gamm
  * logp     [N] fp32.  entropy [N] fp32 or NULL.  top_idx [N, top] int32 and top_logp [N, top] fp32
  *          (required when top > 0).  stats [N, 2] fp32 or NULL, 8-byte aligned.
  * flags    [N] uint32 or NULL, OR'ed with NONFINITE / TOKEN_RANGE / RAGGED_OFFSETS of each entry.
- * Sums are fp32 per lane, joined in fp64; results do not depend on timing.  N = 0 does nothing.
+ * Sums are fp32, per lane and joined pairwise over lanes, warps and CTAs, with one maximum's term held
+ * apart; the logarithm and what follows it are fp64.  Results do not depend on timing.  N = 0 does nothing.
  * Limits: V <= 2^21, N <= 2^26.  No workspace.
  * -------------------------------------------------------------------------- */
 #define DSPARK_TOP_MAX 32
@@ -509,8 +510,8 @@ int dspark_quantize_q8(const void* x, int dtype, int64_t ldx, int M, int d, int8
  * [P1 §"DSpark 架构设计：半自回归生成与马尔可夫修正"] the parallel backbone shares the target's LM head
  * and emits the base logits of every position in one forward.  This is that head on 8-bit weights:
  *     out[m,n] = q_scale[m] * w_scale[n] * sum_k q[m,k] * w[n,k]
- * The sum is exact (int32); it is rounded to fp32 once, multiplied by the scales in fp32 and rounded
- * once to the output's type.  With out fp32 and the rows m in the order of U ([gamma, B] or [B, gamma])
+ * The sum is exact (int32); it is rounded to fp32 once, multiplied by q_scale[m], then by w_scale[n], in
+ * fp32 and rounded once to the output's type.  With out fp32 and the rows m in the order of U ([gamma, B] or [B, gamma])
  * or of l_t, the output is the input of dspark_markov_draft or dspark_verify.
  *
  * q        [M, K] int8, 16-byte aligned, rows ldq bytes apart;  q_scale [M] fp32.
@@ -518,8 +519,8 @@ int dspark_quantize_q8(const void* x, int dtype, int64_t ldx, int M, int d, int8
  *          ldq and ldw are multiples of 16 (bytes between a row's end and the next are not read);
  *          multiples of 128 are read fastest.
  * out      [M, N] of out_dtype (DSPARK_F32, DSPARK_BF16 or DSPARK_F16), rows ldo elements apart.
- * flags    [M] uint32 or NULL: DEVICE_TIMEOUT where a bounded device wait gave up; the outputs it
- *          could not compute are then NaN.
+ * flags    [M] uint32 or NULL: DEVICE_TIMEOUT for each token of which an output could not be computed
+ *          because a bounded device wait gave up; those outputs are NaN.
  * Limits: 1 <= K <= 131071; M, N <= 2^30 and M * N below about 2^39.  out overlaps no input.  M = 0 does nothing.  No workspace.
  * -------------------------------------------------------------------------- */
 int dspark_matmul_q8(const int8_t* q, int64_t ldq, const float* q_scale, const int8_t* w, int64_t ldw,

@@ -9,10 +9,11 @@
 // One CTA per row.  The row stays in registers between the pass that reads it (sum of squares and
 // maximum in one block reduction) and the pass that writes q, so every byte moves once; rows too long
 // or not aligned for that are read again from the stored h.  Bound by HBM: 16384 rows of 5120 bf16 with a
-// residual take 92 us (6.4 TB/s).  What it took to get there is few instructions: with one value at a
-// time the same launch shape measured 127 us, three quarters of its issue slots busy.  A persistent grid
-// that loads a row ahead measured 207 us (the registers of two rows leave too few warps).  Rows of odd
-// length have a form of their own: 5000 x 4095 bf16 42 us, value by value 67 (5000 x 4096: 24).
+// residual take 89 us (6.6 TB/s; the call alone, in a row of calls on rotating inputs).  What it took to get
+// there is few instructions: with one value at a time the same launch shape measured 127 us, three quarters
+// of its issue slots busy.  A persistent grid that loads a row ahead measured 207 us (the registers of two
+// rows leave too few warps).  Rows of odd length have a form of their own: 5000 x 4095 bf16 43 us, value by
+// value 67 (5000 x 4096: 25).
 
 #include <cuda_fp16.h>
 

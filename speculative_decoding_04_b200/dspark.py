@@ -508,7 +508,8 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, T: float = 1.0, *
     int32 of any shape with N values, entry n under row n, or under row rows[n] (int64, as many values
     as tokens).  -1 is an entry without a token.  Returns (logp, entropy, top_idx, top_logp, stats):
     logp and entropy shaped as tokens, the alternatives [..., top] (None when top is 0), stats [..., 2]
-    for token_logprobs_backward.  flags: int32, one word per entry, zeroed by the caller, or None."""
+    for token_logprobs_backward.  flags: int32, one word per entry, zeroed by the caller, or None.
+    Nothing is recorded for autograd: the gradient is token_logprobs_backward's, called by the caller."""
     return _call(_binding.token_logprobs, stream, logits, tokens, T, top, rows, logp, entropy, top_idx, top_logp, stats,
                  flags)
 
