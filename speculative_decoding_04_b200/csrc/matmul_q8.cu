@@ -36,9 +36,9 @@ constexpr int kMqBlocks = 2;  // blocks of K per stage
 constexpr int kMqMaxStages = 8;
 constexpr uint32_t kMqSmem = 227u * 1024u;
 // Tokens of one single-CTA call; more than this: CTA pairs.  (One CTA a tile against pairs, in a row of calls,
-// measured at two large vocabularies only: 151936 x 4096,
-// fp32 out, 40 tokens 101 and 107 us, 80 108 and 113, 84 116 and 112, 100 124 and 117, 128 131 and 122;
-// 129280 x 2048, bf16 out, 64 48 and 49, 84 57 and 50, 128 59 and 55.)
+// measured at two large vocabularies only: 151936 x 4096, fp32 out, 40 tokens 101 and 107 us, 80 108 and 113,
+// 84 116 and 112, 100 124 and 117, 128 131 and 122; 129280 x 2048, bf16 out, 64 48 and 49, 84 57 and 50, 128 59
+// and 55.)
 constexpr int kMqMaxTokens = 80;
 
 struct MqArgs {
@@ -63,8 +63,8 @@ struct MqArgs {
 // Tensor maps of the weights and the tokens: [rows, K] with boxes of 128 bytes of K by the tile's rows,
 // and the same matrix as [K / 128][rows][128 bytes] with boxes of two blocks.  One copy of two blocks
 // streams faster than two of one (single calls behind a flush of L2, when it was chosen: 1088 x 151936 x 4096
-// 485 against 530 us, one token 115 against 121; in a row of calls these take 580-615 and 94 today);
-// the last odd or partial block comes by the first map, which ends at K.
+// 485 against 530 us, one token 115 against 121; in a row of calls they take 580-615 and 94); the last odd or
+// partial block comes by the first map, which ends at K.
 struct MqMaps {
   CUtensorMap w, x, w3, x3;
   CUtensorMap out;  // [M, N] of the output's type in boxes of kOutTokens x 128 (CTA pairs, out_tma)
